@@ -74,7 +74,10 @@ typedef enum mla_status {
   MLA_ERR_WORKSPACE = 5,      /* workspace smaller than the *_workspace_size   */
   MLA_ERR_UNSUPPORTED = 6,    /* valid MLA shape the library does not implement */
   MLA_ERR_CUDA = 7,           /* a CUDA runtime call or launch failed          */
-  MLA_ERR_DEVICE_TIMEOUT = 8  /* a bounded on-device wait gave up (reported by
+  MLA_ERR_DEVICE_TIMEOUT = 8, /* a bounded on-device wait gave up (reported by
+                                 mla_check_device_status)                      */
+  MLA_ERR_NO_BLOCKS = 9       /* mla_paged_plan: more blocks or slots needed
+                                 than there are (reported by
                                  mla_check_device_status)                      */
 } mla_status;
 
@@ -360,11 +363,148 @@ MLA_API mla_status mla_decode_absorbed(const mla_config* cfg, const void* q_nope
                                size_t workspace_bytes, void* stream);
 
 /*
+ * The paged 8-bit latent cache.
+ *
+ * [MEGATRON] 推理优化 keeps one row [kv_compressed | k_pos_emb] per token.
+ * Here the rows of all requests live in one pool of blocks:
+ *   cache   [n_blocks, block_size, kv_lora_rank + rope]  e4m3 bytes
+ *   scales  fp32 [n_blocks], one power of two 2^e per block, -64 <= e <= 120
+ * and the value of a byte is e4m3(byte) * 2^e.  A request's token j lies in
+ * row j % block_size of block block_table[b][j / block_size].  Limits:
+ * block_size 16, 32, 64 or 128; kv_lora_rank + rope a multiple of 16; at most
+ * 8192 requests a call; n_blocks * block_size and max_blocks * block_size
+ * below 2^31 (byte offsets are 64-bit).  Integer arrays, scales and tables
+ * need 4-byte alignment, cache and rows 16, workspaces 256.
+ *
+ * Lengths, block ids, slots and scales are read on the device only.  One that
+ * is out of range never leads outside a buffer: it is replaced or skipped and
+ * the status word says so (mla_check_device_status: MLA_ERR_SHAPE).  Calls on
+ * one workspace share its status word and scratch: calls that may overlap on
+ * the GPU need workspaces of their own.
+ */
+
+/* Workspace bytes of mla_paged_plan, _append and _gather on a pool of
+ * n_blocks blocks; 0 if n_blocks < 1. */
+MLA_API size_t mla_paged_workspace_size(int32_t n_blocks);
+
+/*
+ * mla_paged_plan -- block tables and slot maps of one serving step from the
+ * requests' lengths.
+ *
+ *   held_b = ceil(ctx_b / block_size), want_b = ceil((ctx_b + new_b) / block_size)
+ * A request takes want_b - held_b blocks from the front of the free ring (in
+ * request order); with new_b = -1 it leaves: its held_b blocks go behind the
+ * ring's end, in table order, and can be taken from the next call on.  The
+ * new tokens of all requests are numbered back to back:
+ *   cu_new[b+1] = cu_new[b] + max(new_b, 0)
+ *   positions[cu_new[b] + i] = ctx_b + i
+ *   slot_map[cu_new[b] + i] = block * block_size + row of that position
+ * and entries from cu_new[B] on hold slot -1, position 0.
+ *
+ *   ctx_len      [B] cached tokens
+ *   new_len      [B] new tokens, or -1
+ *   block_table  [B, max_blocks], updated in place; entries past a request's
+ *                blocks are left alone
+ *   free_ring    [n_blocks]; entries head .. head + count - 1 (mod n_blocks)
+ *                are the free blocks; updated in place
+ *   free_state   {head, count}
+ *   ctx_out, free_state_out  lengths and ring state after the step; may be
+ *                ctx_len and free_state themselves
+ *   slot_map, positions  [capacity]; positions may be NULL, both may be when
+ *                capacity is 0
+ *   cu_new       [B + 1]
+ * All or nothing: when the ring or the capacity is too small (status
+ * MLA_ERR_NO_BLOCKS) or a length or the ring's state is out of range
+ * (MLA_ERR_SHAPE), tables, ring, lengths and state stay as they were, cu_new
+ * is zero and every slot is -1.
+ */
+MLA_API mla_status mla_paged_plan(const int32_t* ctx_len, const int32_t* new_len,
+                                  int32_t* block_table, int32_t* free_ring,
+                                  const int32_t* free_state, int32_t* ctx_out,
+                                  int32_t* free_state_out, int32_t* slot_map,
+                                  int32_t* positions, int32_t* cu_new, int32_t B,
+                                  int32_t max_blocks, int32_t n_blocks, int32_t block_size,
+                                  int32_t capacity, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * mla_paged_append -- quantise latent rows into the blocks a slot map names.
+ *
+ *   rows      [n_rows, kv_lora_rank + rope] in cfg->dtype, as latent_cache_out
+ *             of a prefill gives them
+ *   slot_map  [n_rows]; -1 skips a row
+ * Rows whose slots follow one another inside a block form a run (a block takes
+ * one run a call).  With e_new the smallest e >= -64 such that
+ * max |v| <= 448 * 2^e over the run's finite values, the block's scale becomes
+ *   2^e,  e = e_new          if the run starts at row 0 of the block
+ *         e = max(e_new, e_old)  otherwise: rows in front of the run are kept,
+ *                             e4m3(old * 2^(e_old - e))
+ * and the run's rows e4m3(v * 2^-e), to nearest, ties to even.  An infinity or
+ * NaN becomes NaN.  Rows of the block behind the run are not touched, and are
+ * dead: write a block front to back.
+ * A slot outside the pool, a slot in the block of the slot before it that does
+ * not follow it, and a second run in one block (which of the two is not
+ * specified) are skipped and reported as MLA_ERR_SHAPE.
+ */
+MLA_API mla_status mla_paged_append(const mla_config* cfg, const void* rows,
+                                    const int32_t* slot_map, void* cache, float* scales,
+                                    int32_t n_rows, int32_t n_blocks, int32_t block_size,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mla_paged_gather -- the cached rows of all requests back to back in
+ * cfg->dtype (the history a chunked prefill uncompresses, or a contiguous
+ * cache for mla_decode_absorbed).
+ *
+ *   rows_out  [capacity, kv_lora_rank + rope]: row cu_ctx[b] + j is token j of
+ *             request b; rows from cu_ctx[B] on are left alone.  NULL when
+ *             capacity is 0
+ *   cu_ctx    [B + 1], written
+ * Rows beyond the capacity are not written and a row whose block id is out of
+ * range is zero; both are reported as MLA_ERR_SHAPE, and so is a length
+ * outside [0, max_blocks * block_size], which is clamped.
+ */
+MLA_API mla_status mla_paged_gather(const mla_config* cfg, const void* cache, const float* scales,
+                                    const int32_t* block_table, const int32_t* ctx_len,
+                                    void* rows_out, int32_t* cu_ctx, int32_t B,
+                                    int32_t max_blocks, int32_t n_blocks, int32_t block_size,
+                                    int32_t capacity, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* Byte offsets of the paged decode's intermediates inside the workspace. */
+typedef struct mla_paged_layout {
+  int64_t status, q_lat, part_o, part_lse, o_lat, o, total_bytes;
+  int32_t split_tokens, max_splits;
+} mla_paged_layout;
+
+/* Workspace bytes mla_decode_paged needs; 0 if the arguments are invalid. */
+MLA_API size_t mla_decode_paged_workspace_size(const mla_config* cfg, int32_t B,
+                                               int32_t max_blocks, int32_t block_size,
+                                               mla_paged_layout* layout);
+
+/*
+ * mla_decode_paged -- mla_decode_absorbed over the paged 8-bit cache: one
+ * query token per request against the ctx_len[b] rows of its blocks.
+ *
+ *   q_nope, q_pe, w_kv_b, w_o, out   as in mla_decode_absorbed
+ *   block_table  [B, max_blocks];  ctx_len [B], counting the current token; a
+ *                request without tokens (ctx_len 0) gets a zero row
+ * Rows of a block behind the last token are never used, whatever they hold.
+ */
+MLA_API mla_status mla_decode_paged(const mla_config* cfg, const void* q_nope, const void* q_pe,
+                                    const void* w_kv_b, const void* cache, const float* scales,
+                                    const int32_t* block_table, const int32_t* ctx_len, int32_t B,
+                                    int32_t max_blocks, int32_t n_blocks, int32_t block_size,
+                                    const void* w_o, void* out, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
  * mla_check_device_status -- synchronise `stream`, read the status word that
- * the last prefill/decode call on this workspace left at its start, and clear
- * it.  Returns MLA_OK, MLA_ERR_DEVICE_TIMEOUT (a bounded mbarrier or flag
+ * the last prefill/decode/paged call on this workspace left at its start, and
+ * clear it.  Returns MLA_OK, MLA_ERR_DEVICE_TIMEOUT (a bounded mbarrier or flag
  * wait in a kernel ran out and the kernel returned early; its outputs are
- * invalid) or MLA_ERR_SHAPE (decode saw a cu_ctx entry out of range).
+ * invalid), MLA_ERR_NO_BLOCKS (mla_paged_plan) or MLA_ERR_SHAPE (a cu_ctx,
+ * cu_seqlens, length, block id, slot or scale out of range).
  * workspace is a device pointer; this call blocks the host.
  */
 MLA_API mla_status mla_check_device_status(void* workspace, void* stream);

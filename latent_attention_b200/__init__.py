@@ -15,7 +15,8 @@ import ctypes as C
 
 from . import _lib
 from ._lib import (mla_config, mla_weights, mla_prefill_layout,
-                   mla_decode_layout, MLA_F32, MLA_BF16, ROPE_TYPES)
+                   mla_decode_layout, mla_paged_layout, MLA_F32, MLA_BF16,
+                   ROPE_TYPES)
 
 __all__ = ["MlaError", "make_config", "mla_build_rope_tables",
            "mla_prefill_workspace_size", "mla_prefill_forward",
@@ -23,7 +24,9 @@ __all__ = ["MlaError", "make_config", "mla_build_rope_tables",
            "mla_check_device_status", "mla_decode_absorbed_noalloc",
            "mla_prefill_chunked_workspace_size", "mla_prefill_chunked",
            "mla_prefill_varlen_workspace_size", "mla_prefill_varlen",
-           "abi_version"]
+           "mla_paged_workspace_size", "mla_paged_plan", "mla_paged_append",
+           "mla_paged_gather", "mla_decode_paged_workspace_size",
+           "mla_decode_paged", "abi_version"]
 
 
 class MlaError(RuntimeError):
@@ -275,4 +278,113 @@ def mla_decode_absorbed_noalloc(cfg, q_nope, q_pe, w_kv_b, latent_cache, cu_ctx,
                                                    cu_ctx, B, w_o, out)
     _check(_lib.load().mla_decode_absorbed_noalloc(
         C.byref(c), qn, qp, wkvb, cache, cu, int(B), int(max_ctx), wo, o,
+        _stream(stream)))
+
+
+# ------------------------------------------------- the paged 8-bit cache
+def mla_paged_workspace_size(n_blocks):
+    n = _lib.load().mla_paged_workspace_size(int(n_blocks))
+    if n == 0:
+        raise MlaError(2, f"n_blocks={n_blocks}")
+    return n
+
+
+def _ws(workspace, *tensors):
+    """The workspace pair, after checking that every tensor of the call lies on
+    the workspace's device and that this is the current one (the kernels launch
+    there)."""
+    import torch
+    p, dev = _ptr(workspace, "workspace"), workspace.device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {t.device} and workspace on {dev}")
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return p, C.c_size_t(workspace.numel() * workspace.element_size())
+
+
+def _pool_ptrs(c, cache, scales, n_blocks, block_size):
+    """The pool's blocks (e4m3, or their bytes as uint8) and scales."""
+    import torch
+    dt = torch.uint8 if cache is not None and cache.dtype == torch.uint8 else torch.float8_e4m3fn
+    n = int(n_blocks) * int(block_size) * (c.kv_lora_rank + c.qk_rope_head_dim)
+    return (_ptr(cache, "cache", False, dt, n),
+            _ptr(scales, "scales", False, _f32(), int(n_blocks)))
+
+
+def mla_paged_plan(ctx_len, new_len, block_table, free_ring, free_state, ctx_out, free_state_out,
+                   slot_map, positions, cu_new, B, max_blocks, n_blocks, block_size, capacity,
+                   workspace, stream=None):
+    """Block tables and slot maps of one step (all int32 device tensors);
+    ``positions`` may be None, and ``slot_map`` too when ``capacity`` is 0."""
+    i32, B, cap = _i32(), int(B), int(capacity)
+    _check(_lib.load().mla_paged_plan(
+        _ptr(ctx_len, "ctx_len", False, i32, B), _ptr(new_len, "new_len", False, i32, B),
+        _ptr(block_table, "block_table", False, i32, B * int(max_blocks)),
+        _ptr(free_ring, "free_ring", False, i32, int(n_blocks)),
+        _ptr(free_state, "free_state", False, i32, 2), _ptr(ctx_out, "ctx_out", False, i32, B),
+        _ptr(free_state_out, "free_state_out", False, i32, 2),
+        _ptr(slot_map, "slot_map", cap == 0, i32, cap),
+        _ptr(positions, "positions", True, i32, cap), _ptr(cu_new, "cu_new", False, i32, B + 1),
+        B, int(max_blocks), int(n_blocks), int(block_size), cap,
+        *_ws(workspace, ctx_len, new_len, block_table, free_ring, free_state, ctx_out,
+             free_state_out, slot_map, positions, cu_new), _stream(stream)))
+
+
+def mla_paged_append(cfg, rows, slot_map, cache, scales, n_rows, n_blocks, block_size, workspace,
+                     stream=None):
+    """Quantise ``rows`` [n_rows, kv_lora_rank + rope] into the slots of
+    ``slot_map`` (-1: skip)."""
+    c = cfg if isinstance(cfg, mla_config) else make_config(cfg)
+    n, row = int(n_rows), c.kv_lora_rank + c.qk_rope_head_dim
+    _check(_lib.load().mla_paged_append(
+        C.byref(c), _ptr(rows, "rows", False, _dt(c), n * row),
+        _ptr(slot_map, "slot_map", False, _i32(), n),
+        *_pool_ptrs(c, cache, scales, n_blocks, block_size), n, int(n_blocks), int(block_size),
+        *_ws(workspace, rows, slot_map, cache, scales), _stream(stream)))
+
+
+def mla_paged_gather(cfg, cache, scales, block_table, ctx_len, rows_out, cu_ctx, B, max_blocks,
+                     n_blocks, block_size, capacity, workspace, stream=None):
+    """Rows of all requests back to back into ``rows_out`` [capacity, ...],
+    their prefix sums into ``cu_ctx`` [B + 1]."""
+    c = cfg if isinstance(cfg, mla_config) else make_config(cfg)
+    B, cap, row = int(B), int(capacity), c.kv_lora_rank + c.qk_rope_head_dim
+    _check(_lib.load().mla_paged_gather(
+        C.byref(c), *_pool_ptrs(c, cache, scales, n_blocks, block_size),
+        _ptr(block_table, "block_table", False, _i32(), B * int(max_blocks)),
+        _ptr(ctx_len, "ctx_len", False, _i32(), B),
+        _ptr(rows_out, "rows_out", cap == 0, _dt(c), cap * row),
+        _ptr(cu_ctx, "cu_ctx", False, _i32(), B + 1), B, int(max_blocks), int(n_blocks),
+        int(block_size), cap, *_ws(workspace, cache, scales, block_table, ctx_len, rows_out,
+                                   cu_ctx), _stream(stream)))
+
+
+def mla_decode_paged_workspace_size(cfg, B, max_blocks, block_size):
+    c = cfg if isinstance(cfg, mla_config) else make_config(cfg)
+    lay = mla_paged_layout()
+    n = _lib.load().mla_decode_paged_workspace_size(C.byref(c), int(B), int(max_blocks),
+                                                    int(block_size), C.byref(lay))
+    if n == 0:
+        raise MlaError(2, "invalid configuration or sizes")
+    return n, {f: getattr(lay, f) for f, _ in lay._fields_}
+
+
+def mla_decode_paged(cfg, q_nope, q_pe, w_kv_b, cache, scales, block_table, ctx_len, B,
+                     max_blocks, n_blocks, block_size, w_o, out, workspace, stream=None):
+    """One query token per request over the blocks of its table."""
+    c = cfg if isinstance(cfg, mla_config) else make_config(cfg)
+    B, h, r, dt = int(B), c.num_heads, c.kv_lora_rank, _dt(c)
+    dn, dr, dv, H = c.qk_nope_head_dim, c.qk_rope_head_dim, c.v_head_dim, c.hidden_size
+    _check(_lib.load().mla_decode_paged(
+        C.byref(c), _ptr(q_nope, "q_nope", False, dt, B * h * dn),
+        _ptr(q_pe, "q_pe", False, dt, B * h * dr),
+        _ptr(w_kv_b, "w_kv_b", False, dt, h * (dn + dv) * r),
+        *_pool_ptrs(c, cache, scales, n_blocks, block_size),
+        _ptr(block_table, "block_table", False, _i32(), B * int(max_blocks)),
+        _ptr(ctx_len, "ctx_len", False, _i32(), B), B, int(max_blocks), int(n_blocks),
+        int(block_size), _ptr(w_o, "w_o", True, dt, H * h * dv),
+        _ptr(out, "out", False, dt, B * (H if w_o is not None else h * dv)),
+        *_ws(workspace, q_nope, q_pe, w_kv_b, cache, scales, block_table, ctx_len, w_o, out),
         _stream(stream)))

@@ -16,7 +16,7 @@ MLA_OK = 0
 STATUS_NAMES = {0: "MLA_OK", 1: "MLA_ERR_NULL", 2: "MLA_ERR_SHAPE",
                 3: "MLA_ERR_ALIGN", 4: "MLA_ERR_DTYPE", 5: "MLA_ERR_WORKSPACE",
                 6: "MLA_ERR_UNSUPPORTED", 7: "MLA_ERR_CUDA",
-                8: "MLA_ERR_DEVICE_TIMEOUT"}
+                8: "MLA_ERR_DEVICE_TIMEOUT", 9: "MLA_ERR_NO_BLOCKS"}
 MLA_F32, MLA_BF16 = 0, 1
 # Size of the library's static decode scratch (mla.h MLA_DECODE_NOALLOC_SCRATCH_BYTES).
 DECODE_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -30,7 +30,9 @@ EXPORTED = ["mla_abi_version", "mla_status_string", "mla_last_error_detail",
             "mla_set_stage_events", "mla_kernel_launches",
             "mla_decode_absorbed_noalloc", "mla_selftest_wait_timeout",
             "mla_prefill_chunked_workspace_size", "mla_prefill_chunked",
-            "mla_prefill_varlen_workspace_size", "mla_prefill_varlen"]
+            "mla_prefill_varlen_workspace_size", "mla_prefill_varlen",
+            "mla_paged_workspace_size", "mla_paged_plan", "mla_paged_append",
+            "mla_paged_gather", "mla_decode_paged_workspace_size", "mla_decode_paged"]
 
 
 class mla_config(C.Structure):
@@ -59,6 +61,13 @@ class mla_prefill_layout(C.Structure):
 
 
 class mla_decode_layout(C.Structure):
+    _fields_ = [(n, C.c_int64) for n in
+                ("status", "q_lat", "part_o", "part_lse", "o_lat", "o",
+                 "total_bytes")] + [("split_tokens", C.c_int32),
+                                    ("max_splits", C.c_int32)]
+
+
+class mla_paged_layout(C.Structure):
     _fields_ = [(n, C.c_int64) for n in
                 ("status", "q_lat", "part_o", "part_lse", "o_lat", "o",
                  "total_bytes")] + [("split_tokens", C.c_int32),
@@ -123,5 +132,18 @@ def load():
     lib.mla_decode_absorbed_noalloc.restype = C.c_int
     lib.mla_decode_absorbed_noalloc.argtypes = [cfgp, vp, vp, vp, vp, vp, i32, i32, vp,
                                                 vp, vp]
+    lib.mla_paged_workspace_size.restype = sz
+    lib.mla_paged_workspace_size.argtypes = [i32]
+    lib.mla_paged_plan.restype = C.c_int
+    lib.mla_paged_plan.argtypes = [vp] * 10 + [i32] * 5 + [vp, sz, vp]
+    lib.mla_paged_append.restype = C.c_int
+    lib.mla_paged_append.argtypes = [cfgp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]
+    lib.mla_paged_gather.restype = C.c_int
+    lib.mla_paged_gather.argtypes = [cfgp] + [vp] * 6 + [i32] * 5 + [vp, sz, vp]
+    lib.mla_decode_paged_workspace_size.restype = sz
+    lib.mla_decode_paged_workspace_size.argtypes = [cfgp, i32, i32, i32,
+                                                    C.POINTER(mla_paged_layout)]
+    lib.mla_decode_paged.restype = C.c_int
+    lib.mla_decode_paged.argtypes = [cfgp] + [vp] * 7 + [i32] * 4 + [vp, vp, vp, sz, vp]
     _lib = lib
     return lib

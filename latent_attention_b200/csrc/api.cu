@@ -19,7 +19,10 @@ thread_local cudaEvent_t g_events[8];
 thread_local int g_n_events = 0;
 std::atomic<int64_t> g_launches{0};
 
-mla_status fail(mla_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+}  // namespace
+
+namespace mla {
+
 mla_status fail(mla_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -34,10 +37,7 @@ mla_status cuda_fail(cudaError_t e, const char* what) {
   return fail(MLA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
-
-double yarn_m(double s, double a) { return s <= 1.0 ? 1.0 : 0.1 * a * std::log(s) + 1.0; }
+static double yarn_m(double s, double a) { return s <= 1.0 ? 1.0 : 0.1 * a * std::log(s) + 1.0; }
 
 // Softmax scale of the CSDN DeepseekV3Attention __init__ (and Megatron's
 // mscale*mscale/sqrt(q_head_dim)); Kimi uses the plain q_head_dim^-0.5.
@@ -50,8 +50,6 @@ double softmax_scale(const mla_config& c) {
   }
   return s;
 }
-
-int elem_size(const mla_config& c) { return c.dtype == MLA_F32 ? 4 : 2; }
 
 mla_status check_config(const mla_config* c) {
   if (!c) return fail(MLA_ERR_NULL, "cfg is NULL");
@@ -83,6 +81,34 @@ mla_status check_config(const mla_config* c) {
   if (!(c->rms_eps >= 0.0)) return fail(MLA_ERR_SHAPE, "rms_eps=%g", c->rms_eps);
   return MLA_OK;
 }
+
+int device_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = 148;
+  }
+  return n;
+}
+
+mla_status succeed() {
+  g_detail.clear();
+  return MLA_OK;
+}
+
+}  // namespace mla
+
+namespace {
+
+using mla::align256;
+using mla::aligned16;
+using mla::check_config;
+using mla::cuda_fail;
+using mla::device_sms;
+using mla::elem_size;
+using mla::fail;
+using mla::softmax_scale;
 
 // The CUDA-core GEMM keeps each rope pair inside one 64-column tile.
 bool rope_fits_simt_tiles(int period, int start, int dr, int count) {
@@ -121,16 +147,6 @@ void prefill_layout(const mla_config& c, int B, int T, int T_past, mla_prefill_l
   L->attn = take(N * c.num_heads * c.v_head_dim * es);
   L->pos = packed ? take(N * 4) : -1;
   L->total_bytes = off;
-}
-
-int device_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-    cudaGetLastError();
-    n = 148;
-  }
-  return n;
 }
 
 // Decode partitions.  Tensor cores: one CTA pair per two SMs, each taking an
@@ -423,6 +439,7 @@ const char* mla_status_string(mla_status s) {
     case MLA_ERR_UNSUPPORTED: return "MLA_ERR_UNSUPPORTED";
     case MLA_ERR_CUDA: return "MLA_ERR_CUDA";
     case MLA_ERR_DEVICE_TIMEOUT: return "MLA_ERR_DEVICE_TIMEOUT";
+    case MLA_ERR_NO_BLOCKS: return "MLA_ERR_NO_BLOCKS";
   }
   return "MLA_ERR_<unknown>";
 }
@@ -594,6 +611,10 @@ mla_status mla_check_device_status(void* workspace, void* stream) {
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(e, "status read");
   if (word & mla::kStatusTimeout) return fail(MLA_ERR_DEVICE_TIMEOUT, "status word 0x%x", word);
+  if (word & mla::kStatusNoBlocks)
+    return fail(MLA_ERR_NO_BLOCKS, "the plan ran out of free blocks or slots (0x%x)", word);
+  if (word & mla::kStatusBadPage)
+    return fail(MLA_ERR_SHAPE, "paged cache: length, block, slot or scale out of range (0x%x)", word);
   if (word & mla::kStatusBadCtx) return fail(MLA_ERR_SHAPE, "cu_ctx / cu_seqlens out of range (0x%x)", word);
   g_detail.clear();
   return MLA_OK;

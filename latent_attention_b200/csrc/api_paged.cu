@@ -1,0 +1,264 @@
+// Host side of the paged 8-bit latent cache: argument validation, workspace
+// layout and launches of mla_paged_* and mla_decode_paged.
+#include <algorithm>
+
+#include "internal.h"
+#include "tc.h"
+
+namespace {
+
+using mla::align256;
+using mla::aligned16;
+using mla::cuda_fail;
+using mla::fail;
+using mla::kMaxRequests;
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// n_blocks and block_size of a pool.
+mla_status check_pool(int32_t n_blocks, int32_t block_size) {
+  if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128)
+    return fail(MLA_ERR_SHAPE, "block_size=%d is not 16, 32, 64 or 128", block_size);
+  if (n_blocks < 1 || (int64_t)n_blocks * block_size >= (1ll << 31))
+    return fail(MLA_ERR_SHAPE, "n_blocks=%d: n_blocks x block_size must be in [1, 2^31)", n_blocks);
+  return MLA_OK;
+}
+
+mla_status check_table(int32_t B, int32_t max_blocks, int32_t block_size) {
+  if (B < 1 || B > kMaxRequests)
+    return fail(MLA_ERR_SHAPE, "B=%d outside [1, %d]", B, kMaxRequests);
+  if (max_blocks < 1 || (int64_t)max_blocks * block_size >= (1ll << 31))
+    return fail(MLA_ERR_SHAPE, "max_blocks=%d: max_blocks x block_size must be in [1, 2^31)",
+                max_blocks);
+  return MLA_OK;
+}
+
+mla_status check_row(const mla_config& c) {
+  if ((c.kv_lora_rank + c.qk_rope_head_dim) % 16)
+    return fail(MLA_ERR_UNSUPPORTED,
+                "paged cache rows (kv_lora_rank + qk_rope_head_dim = %d) must be a multiple of 16",
+                c.kv_lora_rank + c.qk_rope_head_dim);
+  return MLA_OK;
+}
+
+mla_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (reinterpret_cast<uintptr_t>(ws) & 255u)
+    return fail(MLA_ERR_ALIGN, "workspace is not 256-byte aligned");
+  if (have < need) return fail(MLA_ERR_WORKSPACE, "workspace %zu < %zu bytes", have, need);
+  return MLA_OK;
+}
+
+mla::PagedPool pool_of(const mla_config& c, const void* cache, const float* scales, int n_blocks,
+                       int bs) {
+  mla::PagedPool p;
+  p.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
+  p.scales = const_cast<float*>(scales);
+  p.n_blocks = n_blocks;
+  p.bs = bs;
+  p.W = c.kv_lora_rank + c.qk_rope_head_dim;
+  return p;
+}
+
+constexpr int kSimtSplit = 1024;      // tokens per split on CUDA cores
+
+void paged_layout(const mla_config& c, int B, int max_blocks, int block_size,
+                  mla_paged_layout* L) {
+  const int64_t es = mla::elem_size(c), h = c.num_heads, r = c.kv_lora_rank;
+  const int64_t w = r + c.qk_rope_head_dim;
+  int64_t off = 0;
+  auto take = [&](int64_t bytes) { int64_t o = off; off = align256(off + bytes); return o; };
+  const int64_t max_ctx = (int64_t)max_blocks * block_size;
+  L->split_tokens = kSimtSplit;
+  L->max_splits = (int32_t)((max_ctx + kSimtSplit - 1) / kSimtSplit);
+  const int64_t parts = (int64_t)B * L->max_splits;
+  L->status = take(256);
+  L->q_lat = take(B * h * w * es);
+  L->part_o = take(parts * h * r * 4);
+  L->part_lse = take(parts * h * 4);
+  L->o_lat = take(B * h * r * es);
+  L->o = take(B * h * c.v_head_dim * es);
+  L->total_bytes = off;
+}
+
+// Configuration limits of the paged decode.
+mla_status check_decode(const mla_config& c, bool o_proj, int max_blocks, int block_size) {
+  mla_status s = check_row(c);
+  if (s != MLA_OK) return s;
+  const int w = c.kv_lora_rank + c.qk_rope_head_dim;
+  if (std::max(mla::paged_simt_smem(w, kSimtSplit), 4 * c.kv_lora_rank) > mla::kMaxSmem)
+    return fail(MLA_ERR_UNSUPPORTED, "paged decode: kv_lora_rank + qk_rope_head_dim = %d is too large", w);
+  if ((int64_t)max_blocks * block_size > 65535ll * kSimtSplit)
+    return fail(MLA_ERR_UNSUPPORTED, "paged decode: max_blocks x block_size > %lld tokens",
+                65535ll * kSimtSplit);
+  return MLA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mla_paged_workspace_size(int32_t n_blocks) {
+  if (n_blocks < 1) return 0;
+  return (size_t)align256(256 + 4 * (((int64_t)n_blocks + 31) / 32));
+}
+
+mla_status mla_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t* block_table,
+                          int32_t* free_ring, const int32_t* free_state, int32_t* ctx_out,
+                          int32_t* free_state_out, int32_t* slot_map, int32_t* positions,
+                          int32_t* cu_new, int32_t B, int32_t max_blocks, int32_t n_blocks,
+                          int32_t block_size, int32_t capacity, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if (!ctx_len || !new_len || !block_table || !free_ring || !free_state || !ctx_out ||
+      !free_state_out || !cu_new || !workspace || (capacity > 0 && !slot_map))
+    return fail(MLA_ERR_NULL, "a required plan pointer is NULL");
+  mla_status s = check_pool(n_blocks, block_size);
+  if (s == MLA_OK) s = check_table(B, max_blocks, block_size);
+  if (s != MLA_OK) return s;
+  if (capacity < 0) return fail(MLA_ERR_SHAPE, "capacity=%d", capacity);
+  const void* ptrs[] = {ctx_len, new_len, block_table, free_ring, free_state, ctx_out,
+                        free_state_out, slot_map, positions, cu_new};
+  for (const void* p : ptrs)
+    if (p && !aligned4(p)) return fail(MLA_ERR_ALIGN, "pointer %p is not 4-byte aligned", p);
+  s = check_workspace(workspace, workspace_bytes, 256);
+  if (s != MLA_OK) return s;
+  mla::PlanArgs a{ctx_len, new_len, block_table, free_ring, free_state, ctx_out, free_state_out,
+                  slot_map, positions, cu_new, B, max_blocks, n_blocks, block_size, capacity,
+                  static_cast<uint32_t*>(workspace)};
+  const cudaError_t e = mla::launch_paged_plan(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "paged plan");
+  return mla::succeed();
+}
+
+mla_status mla_paged_append(const mla_config* cfg, const void* rows, const int32_t* slot_map,
+                            void* cache, float* scales, int32_t n_rows, int32_t n_blocks,
+                            int32_t block_size, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  mla_status s = mla::check_config(cfg);
+  if (s != MLA_OK) return s;
+  if (!rows || !slot_map || !cache || !scales || !workspace)
+    return fail(MLA_ERR_NULL, "a required append pointer is NULL");
+  s = check_pool(n_blocks, block_size);
+  if (s == MLA_OK) s = check_row(*cfg);
+  if (s != MLA_OK) return s;
+  if (n_rows < 1) return fail(MLA_ERR_SHAPE, "n_rows=%d", n_rows);
+  if (!aligned16(rows) || !aligned16(cache))
+    return fail(MLA_ERR_ALIGN, "rows or cache is not 16-byte aligned");
+  if (!aligned4(slot_map) || !aligned4(scales))
+    return fail(MLA_ERR_ALIGN, "slot_map or scales is not 4-byte aligned");
+  const size_t need = mla_paged_workspace_size(n_blocks);
+  s = check_workspace(workspace, workspace_bytes, need);
+  if (s != MLA_OK) return s;
+  cudaStream_t st = (cudaStream_t)stream;
+  // the status word and the bit per block that claims it for one run
+  cudaError_t e = cudaMemsetAsync(workspace, 0, need, st);
+  if (e != cudaSuccess) return cuda_fail(e, "memset");
+  uint32_t* ws = static_cast<uint32_t*>(workspace);
+  e = mla::launch_paged_append(cfg->dtype, rows, slot_map, n_rows,
+                               pool_of(*cfg, cache, scales, n_blocks, block_size), ws, ws + 64, st);
+  if (e != cudaSuccess) return cuda_fail(e, "paged append");
+  return mla::succeed();
+}
+
+mla_status mla_paged_gather(const mla_config* cfg, const void* cache, const float* scales,
+                            const int32_t* block_table, const int32_t* ctx_len, void* rows_out,
+                            int32_t* cu_ctx, int32_t B, int32_t max_blocks, int32_t n_blocks,
+                            int32_t block_size, int32_t capacity, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  mla_status s = mla::check_config(cfg);
+  if (s != MLA_OK) return s;
+  if (!cache || !scales || !block_table || !ctx_len || !cu_ctx || !workspace ||
+      (capacity > 0 && !rows_out))
+    return fail(MLA_ERR_NULL, "a required gather pointer is NULL");
+  s = check_pool(n_blocks, block_size);
+  if (s == MLA_OK) s = check_table(B, max_blocks, block_size);
+  if (s == MLA_OK) s = check_row(*cfg);
+  if (s != MLA_OK) return s;
+  if (capacity < 0) return fail(MLA_ERR_SHAPE, "capacity=%d", capacity);
+  if (!aligned16(cache) || !aligned16(rows_out))
+    return fail(MLA_ERR_ALIGN, "cache or rows_out is not 16-byte aligned");
+  if (!aligned4(scales) || !aligned4(block_table) || !aligned4(ctx_len) || !aligned4(cu_ctx))
+    return fail(MLA_ERR_ALIGN, "scales, block_table, ctx_len or cu_ctx is not 4-byte aligned");
+  s = check_workspace(workspace, workspace_bytes, 256);
+  if (s != MLA_OK) return s;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaMemsetAsync(workspace, 0, 256, st);
+  if (e != cudaSuccess) return cuda_fail(e, "memset");
+  e = mla::launch_paged_gather(cfg->dtype, pool_of(*cfg, cache, scales, n_blocks, block_size),
+                               block_table, ctx_len, rows_out, cu_ctx, B, max_blocks, capacity,
+                               static_cast<uint32_t*>(workspace), st);
+  if (e != cudaSuccess) return cuda_fail(e, "paged gather");
+  return mla::succeed();
+}
+
+size_t mla_decode_paged_workspace_size(const mla_config* cfg, int32_t B, int32_t max_blocks,
+                                       int32_t block_size, mla_paged_layout* layout) {
+  if (mla::check_config(cfg) != MLA_OK || check_pool(1, block_size) != MLA_OK ||
+      check_table(B, max_blocks, block_size) != MLA_OK ||
+      check_decode(*cfg, false, max_blocks, block_size) != MLA_OK)
+    return 0;
+  mla_paged_layout L;
+  paged_layout(*cfg, B, max_blocks, block_size, &L);
+  if (layout) *layout = L;
+  return (size_t)L.total_bytes;
+}
+
+mla_status mla_decode_paged(const mla_config* cfg, const void* q_nope, const void* q_pe,
+                            const void* w_kv_b, const void* cache, const float* scales,
+                            const int32_t* block_table, const int32_t* ctx_len, int32_t B,
+                            int32_t max_blocks, int32_t n_blocks, int32_t block_size,
+                            const void* w_o, void* out, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  mla_status s = mla::check_config(cfg);
+  if (s != MLA_OK) return s;
+  const mla_config& c = *cfg;
+  if (!q_nope || !q_pe || !w_kv_b || !cache || !scales || !block_table || !ctx_len || !out ||
+      !workspace)
+    return fail(MLA_ERR_NULL, "a required paged decode pointer is NULL");
+  s = check_pool(n_blocks, block_size);
+  if (s == MLA_OK) s = check_table(B, max_blocks, block_size);
+  if (s == MLA_OK) s = check_decode(c, w_o != nullptr, max_blocks, block_size);
+  if (s != MLA_OK) return s;
+  const void* ptrs[] = {q_nope, q_pe, w_kv_b, cache, w_o, out};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(MLA_ERR_ALIGN, "pointer %p is not 16-byte aligned", p);
+  if (!aligned4(scales) || !aligned4(block_table) || !aligned4(ctx_len))
+    return fail(MLA_ERR_ALIGN, "scales, block_table or ctx_len is not 4-byte aligned");
+  mla_paged_layout L;
+  paged_layout(c, B, max_blocks, block_size, &L);
+  s = check_workspace(workspace, workspace_bytes, (size_t)L.total_bytes);
+  if (s != MLA_OK) return s;
+  cudaStream_t st = (cudaStream_t)stream;
+  char* ws = static_cast<char*>(workspace);
+  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+  if (e != cudaSuccess) return cuda_fail(e, "memset");
+  mla::stage_event(0, st);
+  mla::PagedDecodeArgs a{};
+  a.q_nope = q_nope; a.q_pe = q_pe; a.w_kv_b = w_kv_b;
+  a.pool = pool_of(c, cache, scales, n_blocks, block_size);
+  a.table = block_table; a.ctx = ctx_len;
+  a.B = B; a.max_blocks = max_blocks; a.h = c.num_heads; a.dn = c.qk_nope_head_dim;
+  a.dr = c.qk_rope_head_dim; a.dv = c.v_head_dim; a.r = c.kv_lora_rank;
+  a.scale = (float)mla::softmax_scale(c);
+  a.split_tokens = L.split_tokens; a.max_splits = L.max_splits;
+  a.q_lat = ws + L.q_lat;
+  a.part_o = (float*)(ws + L.part_o); a.part_lse = (float*)(ws + L.part_lse);
+  a.o_lat = ws + L.o_lat;
+  a.o = w_o ? ws + L.o : out;
+  a.status = (uint32_t*)(ws + L.status);
+  e = mla::launch_paged_decode_simt(c.dtype, a, st);
+  if (e != cudaSuccess) return cuda_fail(e, "paged decode");
+  mla::stage_event(4, st);
+  if (w_o) {
+    mla::GemmArgs go;
+    go.A = a.o; go.lda = (int64_t)a.h * a.dv; go.M = B; go.K = a.h * a.dv; go.nseg = 1;
+    go.Bm[0] = w_o; go.ldb[0] = (int64_t)a.h * a.dv;
+    go.seg[0].out = out; go.seg[0].ldo = c.hidden_size; go.seg[0].ncols = c.hidden_size;
+    e = mla::tc_gemm_supported(go, c.dtype) ? mla::tc_gemm(go, st, a.status)
+                                           : mla::launch_gemm_simt(c.dtype, go, st);
+    if (e != cudaSuccess) return cuda_fail(e, "paged decode o_proj");
+  }
+  mla::stage_event(5, st);
+  return mla::succeed();
+}
+
+}  // extern "C"

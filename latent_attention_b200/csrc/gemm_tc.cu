@@ -536,8 +536,6 @@ int num_sms() {
   return n;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 }  // namespace
 
 bool tc_gemm_supported(const GemmArgs& a, int dtype) {

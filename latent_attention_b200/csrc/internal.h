@@ -15,6 +15,8 @@ namespace mla {
 enum : uint32_t {
   kStatusTimeout = 1u << 0,   // a bounded wait ran out
   kStatusBadCtx = 1u << 1,    // a cu_ctx / cu_seqlens length outside its bounds
+  kStatusBadPage = 1u << 2,   // paged cache: a length, block id, slot or scale out of range
+  kStatusNoBlocks = 1u << 3,  // paged cache: the plan needs more blocks or slots than there are
 };
 
 template <typename T> struct Elem;
@@ -121,6 +123,42 @@ struct DecodeArgs {
   uint32_t* status;
 };
 
+// The paged 8-bit latent cache (mla_paged_*): a pool of n_blocks blocks of bs
+// rows of W = r + dr e4m3 values, one power-of-two scale per block.
+struct PagedPool {
+  uint8_t* cache;       // [n_blocks, bs, W]
+  float* scales;        // [n_blocks]
+  int n_blocks, bs, W;
+};
+
+struct PlanArgs {
+  const int32_t *ctx, *fresh;      // [B] cached tokens; new tokens or -1
+  int32_t *table, *ring;           // [B, max_blocks], [n_blocks]
+  const int32_t* state;            // {head, count} of the ring
+  int32_t *ctx_out, *state_out, *slots, *pos, *cu;
+  int B, max_blocks, n_blocks, bs, capacity;
+  uint32_t* status;
+};
+
+// Requests a paged call takes at most: every scan over them fits the shared
+// memory of one block.
+constexpr int kMaxRequests = 8192;
+
+// Weight-absorbed decode over the pool's blocks.
+struct PagedDecodeArgs {
+  const void *q_nope, *q_pe, *w_kv_b;
+  PagedPool pool;
+  const int32_t *table, *ctx;      // [B, max_blocks], [B]
+  int B, max_blocks, h, dn, dr, dv, r;
+  float scale;
+  int split_tokens, max_splits;    // CUDA cores: tokens per split, splits per sequence
+  void* q_lat;                     // [B, h, r + dr]
+  float *part_o, *part_lse;        // [B, max_splits, h, r], [B, max_splits, h]
+  void* o_lat;                     // [B, h, r]
+  void* o;                         // [B, h, dv]
+  uint32_t* status;
+};
+
 // cudaFuncSetAttribute applies to the current device only: set a kernel's
 // dynamic shared-memory limit once per device (devices 0..63).
 inline cudaError_t set_dynamic_smem(const void* kernel, int bytes,
@@ -161,6 +199,18 @@ void count_launches(int n = 1);
 void set_error_detail(const char* msg);
 // Records registered stage event i (if any) on stream st.
 void stage_event(int i, cudaStream_t st);
+// Host checks and sizes shared by the entry points (defined in api.cu): an
+// error status with its detail text, the configuration's self-checks, the
+// softmax scale, the SM count of the current device.
+mla_status fail(mla_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+mla_status cuda_fail(cudaError_t e, const char* what);
+mla_status succeed();
+mla_status check_config(const mla_config* c);
+double softmax_scale(const mla_config& c);
+int device_sms();
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
+inline int elem_size(const mla_config& c) { return c.dtype == MLA_F32 ? 4 : 2; }
 
 // Launchers (return the launch error).
 cudaError_t launch_rope_tables(const mla_config& cfg, int max_pos, float* cos,
@@ -182,6 +232,20 @@ cudaError_t launch_latent_finalize(int dtype, const void* ckv,
                                    int dr, float eps, void* cache,
                                    cudaStream_t st, int T = 1, int dst_T = 1, int dst_off = 0);
 cudaError_t launch_decode_simt(int dtype, const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st);
+cudaError_t launch_paged_append(int dtype, const void* rows, const int32_t* slots, int n_rows,
+                                const PagedPool& pool, uint32_t* status, uint32_t* claims,
+                                cudaStream_t st);
+cudaError_t launch_paged_gather(int dtype, const PagedPool& pool, const int32_t* table,
+                                const int32_t* ctx, void* rows, int32_t* cu, int B,
+                                int max_blocks, int capacity, uint32_t* status, cudaStream_t st);
+// Shared memory of the CUDA-core paged decode: the query, the split's scores
+// and, per 16 tokens, a scale and a block id.
+constexpr int kMaxSmem = 227 * 1024 - 1024;
+inline int paged_simt_smem(int w, int split_tokens) {
+  return 4 * (w + split_tokens + 2 * (split_tokens / 16));
+}
+cudaError_t launch_paged_decode_simt(int dtype, const PagedDecodeArgs& a, cudaStream_t st);
 // Smallest workspace mla_decode_absorbed runs with (one SM pair on tensor cores).
 size_t decode_min_workspace(const mla_config& c, int B, int max_ctx);
 

@@ -1,0 +1,124 @@
+// e4m3 values and power-of-two block scales of the paged latent cache.
+#pragma once
+#include <cstdint>
+
+#include "internal.h"
+
+namespace mla {
+namespace paged {
+
+// Smallest exponent of a block's scale: a block of zeros has 2^-64.  (The
+// largest that fp32 rows can need is 2^120.)
+constexpr int kMinExp = -64;
+
+// Two floats -> two e4m3 bytes (lo in the low byte), nearest even, +-448 at
+// the ends; NaN stays NaN.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+  return to_e4m3x2(a, b) | (to_e4m3x2(c, d) << 16);
+}
+// Two e4m3 bytes -> an fp16 pair (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
+  return r;
+}
+__device__ __forceinline__ void from_e4m3x4(uint32_t v, float (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t h = e4m3x2_to_f16x2(v >> (16 * i));
+    asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\t"
+        "cvt.f32.f16 %1, h;\n\t}"
+        : "=f"(f[2 * i]), "=f"(f[2 * i + 1])
+        : "r"(h));
+  }
+}
+
+// 2^e for e in [-126, 127]; 0 below, 2^127 above.
+__device__ __forceinline__ float pow2(int e) {
+  return e < -126 ? 0.f : __int_as_float((min(e, 127) + 127) << 23);
+}
+
+// Smallest e >= kMinExp with amax <= 448 * 2^e, for the bits of a finite
+// amax = m 2^k, 1 <= m < 2: 448 = 1.75 * 2^8, so e is k - 8 while m <= 1.75
+// and k - 7 above.
+__device__ __forceinline__ int scale_exp(uint32_t amax_bits) {
+  const int k = (int)(amax_bits >> 23) - 127;
+  return max(k - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0), kMinExp);
+}
+
+// Exponent of a block's stored scale; false unless it is a power of two that
+// the append writes (2^-64 .. 2^120).
+__device__ __forceinline__ bool stored_exp(float scale, int* e) {
+  const uint32_t b = __float_as_uint(scale);
+  *e = (int)(b >> 23) - 127;
+  return (b & 0x807fffffu) == 0 && *e >= kMinExp && *e <= 120;
+}
+
+// 16 consecutive elements as floats (16-byte aligned source).
+__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 x = reinterpret_cast<const float4*>(p)[i];
+    v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
+  }
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+      v[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  }
+}
+__device__ __forceinline__ void store16(float* p, const float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<float4*>(p)[i] =
+        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+      w[k] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    reinterpret_cast<uint4*>(p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// 16 e4m3 bytes times a scale.
+__device__ __forceinline__ void dequant16(uint4 c, float s, float (&v)[16]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float f[4];
+    from_e4m3x4(w[i], f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[4 * i + k] = f[k] * s;
+  }
+}
+
+// First index in [0, n) whose inclusive prefix sum `ends` exceeds i.
+__device__ __forceinline__ int request_of(const int32_t* ends, int n, int i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] <= i) lo = mid + 1; else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace paged
+}  // namespace mla

@@ -1,14 +1,18 @@
 """Convenience holders that keep device buffers for repeated calls.
 
 ``MlaPrefill`` and ``MlaDecode`` own the device copies of the weights, the
-RoPE tables and the workspace (torch allocations), and call the C ABI.  They
-do no arithmetic of their own.
+RoPE tables and the workspace (torch allocations), ``MlaPagedCache`` owns the
+paged latent cache and its tables; they call the C ABI and do no arithmetic of
+their own.
 """
 import torch
 
 from . import (make_config, mla_build_rope_tables, mla_prefill_workspace_size,
                mla_prefill_forward, mla_decode_workspace_size,
-               mla_decode_absorbed, mla_check_device_status)
+               mla_decode_absorbed, mla_check_device_status,
+               mla_paged_workspace_size, mla_paged_plan, mla_paged_append,
+               mla_paged_gather, mla_decode_paged_workspace_size,
+               mla_decode_paged)
 
 _WEIGHT_KEYS = ("w_q_a", "g_q_a", "w_q_b", "w_q", "w_kv_a", "g_kv_a", "w_kv_b",
                 "w_o")
@@ -74,3 +78,69 @@ class MlaDecode:
 
     def check_status(self, stream=None):
         mla_check_device_status(self.ws, stream)
+
+
+class MlaPagedCache:
+    """The paged 8-bit latent cache of up to ``max_requests`` requests of
+    ``max_blocks`` blocks each: the pool, the block tables, the free ring and
+    the lengths, all on the device.  One serving step is ``plan`` (blocks and
+    slots of the new tokens), ``append`` (their latent rows) and ``decode`` or
+    ``gather``; nothing in it waits for the device, so a step can be captured
+    into a CUDA graph."""
+
+    def __init__(self, cfg, max_requests, max_blocks, n_blocks, block_size=64, capacity=None,
+                 device="cuda"):
+        self.cfg, self.B, self.max_blocks = cfg, max_requests, max_blocks
+        self.n_blocks, self.block_size = n_blocks, block_size
+        self.capacity = max_requests if capacity is None else capacity
+        self.c = make_config(cfg)
+        self.dtype = _DT[cfg.dtype]
+        self.device = torch.device(device)
+        self.width = cfg.kv_lora_rank + cfg.qk_rope_head_dim
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.cache = torch.zeros(n_blocks, block_size, self.width, dtype=torch.float8_e4m3fn,
+                                 device=self.device)
+        self.scales = torch.ones(n_blocks, dtype=torch.float32, device=self.device)
+        self.table = torch.full((max_requests, max_blocks), -1, **i32)
+        self.ring = torch.arange(n_blocks, **i32)
+        self.state = torch.tensor([0, n_blocks], **i32)
+        self.ctx = torch.zeros(max_requests, **i32)
+        self.slots = torch.empty(self.capacity, **i32)
+        self.positions = torch.empty(self.capacity, **i32)
+        self.cu_new = torch.empty(max_requests + 1, **i32)
+        self.ws = torch.empty(mla_paged_workspace_size(n_blocks), dtype=torch.uint8,
+                              device=self.device)
+        n, self.layout = mla_decode_paged_workspace_size(self.c, max_requests, max_blocks,
+                                                         block_size)
+        self.decode_ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def plan(self, new_len, stream=None):
+        """Blocks and slots of ``new_len`` [B] tokens (int32; -1: the request
+        leaves).  Returns the slot map, the positions and their prefix sums."""
+        mla_paged_plan(self.ctx, new_len, self.table, self.ring, self.state, self.ctx, self.state,
+                       self.slots, self.positions, self.cu_new, self.B, self.max_blocks,
+                       self.n_blocks, self.block_size, self.capacity, self.ws, stream)
+        return self.slots, self.positions, self.cu_new
+
+    def append(self, rows, slots=None, stream=None):
+        """Quantise ``rows`` [n, W] into the planned slots."""
+        mla_paged_append(self.c, rows, self.slots if slots is None else slots, self.cache,
+                         self.scales, rows.shape[0], self.n_blocks, self.block_size, self.ws,
+                         stream)
+
+    def gather(self, rows_out, cu_ctx, stream=None):
+        mla_paged_gather(self.c, self.cache, self.scales, self.table, self.ctx, rows_out, cu_ctx,
+                         self.B, self.max_blocks, self.n_blocks, self.block_size,
+                         rows_out.shape[0], self.ws, stream)
+        return rows_out, cu_ctx
+
+    def decode(self, q_nope, q_pe, w_kv_b, out, w_o=None, stream=None):
+        mla_decode_paged(self.c, q_nope, q_pe, w_kv_b, self.cache, self.scales, self.table,
+                         self.ctx, self.B, self.max_blocks, self.n_blocks, self.block_size, w_o,
+                         out, self.decode_ws, stream)
+        return out
+
+    def check_status(self, stream=None):
+        """The status of the last plan, append or gather, and of the last decode."""
+        mla_check_device_status(self.ws, stream)
+        mla_check_device_status(self.decode_ws, stream)
