@@ -69,7 +69,7 @@ class mla_decode_layout(C.Structure):
 
 class mla_paged_layout(C.Structure):
     _fields_ = [(n, C.c_int64) for n in
-                ("status", "q_lat", "part_o", "part_lse", "o_lat", "o",
+                ("status", "q_lat", "q8", "plan", "part_o", "part_lse", "o_lat", "o",
                  "total_bytes")] + [("split_tokens", C.c_int32),
                                     ("max_splits", C.c_int32)]
 

@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "paged_slices.cuh"
 #include "tc.h"
 
 namespace {
@@ -68,11 +69,24 @@ void paged_layout(const mla_config& c, int B, int max_blocks, int block_size,
   int64_t off = 0;
   auto take = [&](int64_t bytes) { int64_t o = off; off = align256(off + bytes); return o; };
   const int64_t max_ctx = (int64_t)max_blocks * block_size;
-  L->split_tokens = kSimtSplit;
-  L->max_splits = (int32_t)((max_ctx + kSimtSplit - 1) / kSimtSplit);
-  const int64_t parts = (int64_t)B * L->max_splits;
   L->status = take(256);
-  L->q_lat = take(B * h * w * es);
+  int64_t parts;
+  if (mla::tc_paged_supported(c)) {
+    const mla::PagedTcPlan t = mla::tc_paged_plan(c.num_heads, mla::device_sms());
+    const int64_t rows = (int64_t)B * t.groups * t.NH;
+    L->split_tokens = mla::pslices::CT;
+    L->max_splits = 2 * t.n_units;
+    parts = L->max_splits;
+    L->q_lat = take(B * h * r * es);
+    L->q8 = take(rows * 2 * w + rows * 4);     // the terms, then a factor per row
+    L->plan = take(((int64_t)B + 1) * 8 + (int64_t)B * 4);
+  } else {
+    L->split_tokens = kSimtSplit;
+    L->max_splits = (int32_t)((max_ctx + kSimtSplit - 1) / kSimtSplit);
+    parts = (int64_t)B * L->max_splits;
+    L->q_lat = take(B * h * w * es);
+    L->q8 = L->plan = -1;
+  }
   L->part_o = take(parts * h * r * 4);
   L->part_lse = take(parts * h * 4);
   L->o_lat = take(B * h * r * es);
@@ -85,6 +99,7 @@ mla_status check_decode(const mla_config& c, bool o_proj, int max_blocks, int bl
   mla_status s = check_row(c);
   if (s != MLA_OK) return s;
   const int w = c.kv_lora_rank + c.qk_rope_head_dim;
+  if (mla::tc_paged_supported(c)) return MLA_OK;
   if (std::max(mla::paged_simt_smem(w, kSimtSplit), 4 * c.kv_lora_rank) > mla::kMaxSmem)
     return fail(MLA_ERR_UNSUPPORTED, "paged decode: kv_lora_rank + qk_rope_head_dim = %d is too large", w);
   if ((int64_t)max_blocks * block_size > 65535ll * kSimtSplit)
@@ -245,7 +260,18 @@ mla_status mla_decode_paged(const mla_config* cfg, const void* q_nope, const voi
   a.o_lat = ws + L.o_lat;
   a.o = w_o ? ws + L.o : out;
   a.status = (uint32_t*)(ws + L.status);
-  e = mla::launch_paged_decode_simt(c.dtype, a, st);
+  if (mla::tc_paged_supported(c)) {
+    a.tc = mla::tc_paged_plan(a.h, L.max_splits / 2);
+    const int64_t rows = (int64_t)B * a.tc.groups * a.tc.NH;
+    a.tc.n_units = L.max_splits / 2;
+    a.q8 = (uint8_t*)ws + L.q8;
+    a.qf = (float*)(a.q8 + rows * 2 * (a.r + a.dr));
+    a.pre = (int64_t*)(ws + L.plan);
+    a.len = (int32_t*)(a.pre + B + 1);
+    e = mla::tc_paged_decode(a, st);
+  } else {
+    e = mla::launch_paged_decode_simt(c.dtype, a, st);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "paged decode");
   mla::stage_event(4, st);
   if (w_o) {

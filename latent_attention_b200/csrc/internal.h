@@ -144,6 +144,12 @@ struct PlanArgs {
 // memory of one block.
 constexpr int kMaxRequests = 8192;
 
+// Tensor-core paged decode: the heads in `groups` equal groups of hg_heads
+// (padded to NH), n_units slices of the tokens per group.
+struct PagedTcPlan {
+  int groups, hg_heads, NH, n_units;
+};
+
 // Weight-absorbed decode over the pool's blocks.
 struct PagedDecodeArgs {
   const void *q_nope, *q_pe, *w_kv_b;
@@ -157,6 +163,12 @@ struct PagedDecodeArgs {
   void* o_lat;                     // [B, h, r]
   void* o;                         // [B, h, dv]
   uint32_t* status;
+  // tensor cores: q_lat is [B, h, r], the partials [2 n_units, h, ...]
+  PagedTcPlan tc;
+  uint8_t* q8;                     // [B, groups, 2, NH, r + dr] e4m3 terms
+  float* qf;                       // [B, groups, NH]
+  int64_t* pre;                    // [B + 1]
+  int32_t* len;                    // [B]
 };
 
 // cudaFuncSetAttribute applies to the current device only: set a kernel's

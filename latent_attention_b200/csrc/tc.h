@@ -18,5 +18,10 @@ cudaError_t tc_decode(const DecodeArgs& a, cudaStream_t st);
 // Shortest slice of the token stream one CTA pair of the tensor-core decode
 // takes (tokens).
 int tc_decode_min_slice();
+// The paged decode's tensor-core kernel: the shapes it takes, how it divides
+// h heads over `sms` SMs.
+bool tc_paged_supported(const mla_config& c);
+PagedTcPlan tc_paged_plan(int h, int sms);
+cudaError_t tc_paged_decode(const PagedDecodeArgs& a, cudaStream_t st);
 
 }  // namespace mla
