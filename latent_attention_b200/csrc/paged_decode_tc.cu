@@ -23,7 +23,7 @@
 // each, that read the same blocks at about the same time (the second reading
 // comes from L2).
 //
-// Softmax.  A thread is a token; it holds the scores of half of the heads.
+// Softmax.  A thread is a token; it holds the scores of 16 heads.
 // s = raw 2^e_block f_head (log2 units); p = 2^(s - ref_head); its share of a
 // row sum stays in the thread until the segment ends.  ref is the maximum of the
 // segment's first chunk and moves only when a score passes it by 2^kGrow, so
@@ -38,11 +38,12 @@
 // (paged_slices.cuh), one slice per CTA (and head group); a CTA walks its
 // segments with one continuous pipeline.
 //
-// Warps (384 threads): 0 block lookups, L2 prefetch, TMA of the chunks (a ring
-// of 128-dim boxes; one TMA load per block and box); 1 MMA issue; 2 the
-// segment's query, and zeros over the rows behind a sequence's last token (a
-// weight of 0 times whatever lies there could be NaN); 4-11 softmax, two
-// groups of heads.  All waits are bounded; a timeout sets the status word.
+// Warps: 0 and 2 TMA of the chunks (a ring of 128-dim boxes; one load per block
+// and box), 2 also the block lookups and L2 prefetch; 1 the segments' queries
+// and the MMAs of S; 3 the MMAs of PV; from 4 on softmax, groups of 16 (8) heads.  S and
+// PV have a thread each so that neither waits for the other's inputs: PV of a
+// chunk frees the boxes of the next but one.  All waits are bounded; a timeout
+// sets the status word.
 #include "paged.cuh"
 #include "paged_slices.cuh"
 #include "sm100.cuh"
@@ -58,15 +59,16 @@ using namespace sm100;
 constexpr int R = 512, DR = 64, W = R + DR;
 constexpr int BOX = CT * 128;            // 128 tokens x 128 dims, 16 KB
 constexpr int RBOX = CT * DR;            // 128 tokens x 64 rope dims, 8 KB
-constexpr int NTHREADS = 384;
-constexpr int PF = 3;                    // chunks looked up (and prefetched to L2) ahead
+constexpr int GR = 6;                    // lookup ring, chunks
+constexpr int AHEAD = 3;                 // chunks looked up (and prefetched to L2) ahead of loads
 constexpr float kGrow = 24.f;
 
 // Per head-group size NH (heads of a CTA, padded): ring depth, P buffers and
 // score slots as shared memory (227 KB) and TMEM (512 columns) allow.
 template <int NH>
 struct Cfg {
-  static constexpr int HPG = NH / 2;                       // heads per softmax group
+  static constexpr int HPG = NH == 16 ? 8 : 16;            // heads per softmax group
+  static constexpr int NG = NH / HPG, NTHREADS = 128 + 128 * NG;
   // both terms of P side by side (one product of N = 2 NH), or one after the
   // other (N = NH): O^T's 4 x 2 NH columns fit TMEM up to 32 heads
   static constexpr bool STK = NH <= 32;
@@ -91,17 +93,19 @@ template <int NH>
 struct Shared {
   using K = Cfg<NH>;
   uint8_t sf[K::NP][512];                  // ue8m0 scales of P: head n at (n % 32) 16 + (n / 32) 4
-  float hf[64], ref[64], alpha[64];        // per head: score factor, reference, O's factor
-  union {
-    int hmax[2][4][32];
-    float lsum[2][4][32];
+  float hf[64], nref[64], alpha[64];       // per head: score factor, -reference, factor of O
+  union {                                  // per warp and head; barriers part the uses
+    float inv[K::NG][4][K::HPG];           // 2^-k of its P
+    int hmax[K::NG][4][K::HPG];
+    float lsum[K::NG][4][K::HPG];
   };
-  float scl[4][8];                         // block scales of a chunk
+  float scl[GR][8];                        // scales and ids of a chunk's blocks
+  int ids[GR][8];
   uint64_t q_full, q_free, o_done, o_free, c_full[K::NS], c_empty[K::NS], r_full[K::NR],
-      r_empty[K::NR], t_full[4], g_full[4], s_full[K::NSL], s_free[K::NSL], p_full[K::NP],
-      pv_done[K::NP];
+      r_empty[K::NR], g_full[GR], e_full[GR], s_full[K::NSL], s_free[K::NSL],
+      p_full[K::NP], pv_done[K::NP];
   uint32_t tmem_base;
-  int abort_flag;
+  int abort_flag, first;
 };
 template <int NH>
 constexpr int smem_bytes() { return Cfg<NH>::OFF_SH + (int)sizeof(Shared<NH>); }
@@ -156,6 +160,32 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t* r) {
+  static_assert(N == 8 || N == 16, "columns");
+  if (N == 8) tmem_ld8(taddr, r); else tmem_ld16(taddr, r);
+}
+// (d0, d1) *= (a0, a1) in one packed instruction.
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1) {
+  asm("{\n\t.reg .b64 a, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 d, {%0, %1};\n\t"
+      "mul.rn.f32x2 d, d, a;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -343,15 +373,30 @@ __global__ void __launch_bounds__(kQueryThreads) paged_query_kernel(QueryParams 
 }
 
 // ------------------------------------------------------------- P3: attention
+// First sequence whose charged chunks reach past r, by a whole warp: every
+// round narrows the range 32-fold.
+__device__ __forceinline__ int seq_at_warp(const int64_t* pre, int B, int64_t r, int lane) {
+  int lo = 0, n = B;                          // the answer is in [lo, lo + n), or B - 1
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + (lane + 1) * step;   // pre[at]: end of `step` sequences
+    const bool past = at >= lo + n || pre[at] > r;
+    const int first = __ffs(__ballot_sync(0xffffffffu, past)) - 1;
+    const int left = lo + n - (lo + first * step);
+    lo += first * step;
+    n = min(step, left);
+  }
+  return min(lo, B - 1);
+}
+
 template <int NH>
-__global__ void __launch_bounds__(NTHREADS, 1)
+__global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmQr,
                       const __grid_constant__ CUtensorMap tmC,
                       const __grid_constant__ CUtensorMap tmCr,
                       const __grid_constant__ AttnParams p) {
   using K = Cfg<NH>;
-  constexpr int HPG = K::HPG, NS = K::NS, NR = K::NR, NP = K::NP, NSL = K::NSL;
+  constexpr int HPG = K::HPG, NS = K::NS, NR = K::NR, NP = K::NP, NSL = K::NSL, NG = K::NG;
   extern __shared__ __align__(1024) uint8_t smem[];
   Shared<NH>& sh = *reinterpret_cast<Shared<NH>*>(smem + K::OFF_SH);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -366,40 +411,49 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const Slice sl = unit_slice(p.pre, p.B, u, p.n_units, p.min_len);
   if (sl.r0 >= sl.r1) return;
 
-  if (threadIdx.x == 0) {
-    mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_free, 1);
-    mbar_init(&sh.o_done, 1);
-    mbar_init(&sh.o_free, 8);
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&sh.c_full[i], 1);
-      mbar_init(&sh.c_empty[i], 1);
+  if (warp == 0) {
+    if (lane == 0) {
+      mbar_init(&sh.q_full, 1);
+      mbar_init(&sh.q_free, 1);
+      mbar_init(&sh.o_done, 1);
+      mbar_init(&sh.o_free, 4 * NG);
+      for (int i = 0; i < NS; ++i) {
+        mbar_init(&sh.c_full[i], 1);
+        mbar_init(&sh.c_empty[i], 1);
+      }
+      for (int i = 0; i < NR; ++i) {
+        mbar_init(&sh.r_full[i], 1);
+        mbar_init(&sh.r_empty[i], 1);
+      }
+      for (int i = 0; i < GR; ++i) {
+        mbar_init(&sh.g_full[i], 1);
+        mbar_init(&sh.e_full[i], 1);
+      }
+      for (int i = 0; i < NSL; ++i) {
+        mbar_init(&sh.s_full[i], 1);
+        mbar_init(&sh.s_free[i], 4 * NG);
+      }
+      for (int i = 0; i < NP; ++i) {
+        mbar_init(&sh.p_full[i], 4 * NG);
+        mbar_init(&sh.pv_done[i], 1);
+      }
+      sh.abort_flag = 0;
+      fence_barrier_init();
     }
-    for (int i = 0; i < NR; ++i) {
-      mbar_init(&sh.r_full[i], 1);
-      mbar_init(&sh.r_empty[i], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&sh.t_full[i], 1);
-      mbar_init(&sh.g_full[i], 1);
-    }
-    for (int i = 0; i < NSL; ++i) {
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_free[i], 8);
-    }
-    for (int i = 0; i < NP; ++i) {
-      mbar_init(&sh.p_full[i], 8);
-      mbar_init(&sh.pv_done[i], 1);
-    }
-    sh.abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == 1) {
+  } else if (warp == 1) {
     tmem_alloc(&sh.tmem_base, K::TM_COLS);
     tc_fence_before();
+  } else if (warp == 2) {
+    const int b = seq_at_warp(p.pre, p.B, sl.r0, lane);
+    if (lane == 0) sh.first = b;
+  } else if (warp == 3 && lane == 0) {
+    tma_prefetch(&tmC);
+    tma_prefetch(&tmCr);
+    tma_prefetch(&tmQ);
+    tma_prefetch(&tmQr);
   }
   // scales of heads past NH are copied along with the others' and never used
-  for (int i = threadIdx.x; i < NP * 512; i += NTHREADS) (&sh.sf[0][0])[i] = 127;
+  for (int i = threadIdx.x; i < NP * 512; i += K::NTHREADS) (&sh.sf[0][0])[i] = 127;
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sh.tmem_base;
@@ -408,239 +462,225 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tmem_wait_st();
     tc_fence_before();
   }
+  Cursor c;
+  c.start(p.pre, p.B, sl, u, sh.first);
   __syncthreads();
   tc_fence_after();
-
-  Cursor c;
-  c.start(p.pre, p.B, sl, u);
   const auto advance = [&](Cursor& k) { k.next(p.pre, p.B, sl, u); };
 
+  // TMA loads of box a of a chunk's `blocks` blocks (ids in shared memory); a
+  // thread issues one in some 90 cycles, so two warps share them
+  const auto load_box = [&](int a, int slot, int blocks, const int* ids) {
+    mbar_arrive_expect_tx(&sh.c_full[slot], (blocks << p.lbs) * 128);
+    for (int i = 0; i < blocks; ++i)
+      tma_load_2d(smem + K::OFF_C + slot * BOX + (i << p.lbs) * 128, &tmC, 64 * a, ids[i] << p.lbs,
+                  &sh.c_full[slot]);
+  };
+  // after an abort: the copies in flight (one fill a slot at most, of this pass
+  // over the ring before `slot`, of the pass before from it on) land before the
+  // block ends
+  const auto drain = [&](int slot, uint32_t ph) {
+    int given_up = 0;
+    for (int i = 0; i < NS; ++i)
+      mbar_wait(&sh.c_full[i], (i < slot ? ph ^ 1 : ph) & 1, &given_up, nullptr);
+  };
+
   if (warp == 0) {
-    // ---------------- lookups, L2 prefetch, the rings.  Lane i < 128 / bs has
-    // the chunk's block i: its id is loaded PF + 2 chunks ahead, its scale
-    // (and the block itself, into L2) PF + 1 ahead.
-    if (lane == 0) {
-      tma_prefetch(&tmC);
-      tma_prefetch(&tmCr);
+    // ---------------- TMA of the rope boxes and of the first two boxes
+    if (elect_one()) {
+      int slot = 0, rs = 0, g = 0, n = 0;
+      uint32_t ph = 1, rph = 1;               // parities of the empty barriers
+      for (; !c.done; ++g) {
+        if (c.j == 0) n = p.len[c.s.b];
+        const int valid = min(CT, n - (c.s.c0 + c.j) * CT);
+        const int blocks = (valid + p.bs - 1) >> p.lbs;
+        if (!mbar_wait(&sh.g_full[g % GR], (g / GR) & 1, abort_v, p.status)) break;
+        const int* ids = sh.ids[g % GR];
+        // rope first: the scores start with it
+        if (!mbar_wait(&sh.r_empty[rs], rph, abort_v, p.status)) break;
+        mbar_arrive_expect_tx(&sh.r_full[rs], (blocks << p.lbs) * DR);
+        for (int i = 0; i < blocks; ++i)
+          tma_load_2d(smem + K::OFF_R + rs * RBOX + (i << p.lbs) * DR, &tmCr, R / 2,
+                      ids[i] << p.lbs, &sh.r_full[rs]);
+        if (++rs == NR) { rs = 0; rph ^= 1; }
+        if (!mbar_wait(&sh.c_empty[slot], ph, abort_v, p.status)) break;
+        load_box(0, slot, blocks, ids);
+        if (++slot == NS) { slot = 0; ph ^= 1; }
+        if (!mbar_wait(&sh.c_empty[slot], ph, abort_v, p.status)) break;
+        load_box(1, slot, blocks, ids);
+        slot += 3;
+        if (slot >= NS) { slot -= NS; ph ^= 1; }
+        advance(c);
+      }
+      if (*abort_v) drain(slot, ph);
     }
+  } else if (warp == 1) {
+    // ---------------- the segments' queries, S of every chunk
+    if (elect_one()) {
+      int slot = 0, rs = 0, g = 0;
+      uint32_t ph = 0, rph = 0;
+      const uint32_t qb = smem_u32(smem);
+      const uint64_t dq = desc_kmajor_sw128(qb), dqr = desc_kmajor_sw64(qb + 4 * K::QBOX);
+      const uint64_t dc0 = desc_kmajor_sw128(smem_u32(smem + K::OFF_C));
+      const uint64_t dr0 = desc_kmajor_sw64(smem_u32(smem + K::OFF_R));
+      for (bool ok = true; ok && !c.done; ++g) {
+        if (c.j == 0) {
+          if (c.kk > 0 && !mbar_wait(&sh.q_free, (c.kk - 1) & 1, abort_v, p.status)) break;
+          mbar_arrive_expect_tx(&sh.q_full, K::QBYTES);
+          const int y = (c.s.b * p.groups + hg) * 2 * NH;
+          tma_load_2d(smem + 4 * K::QBOX, &tmQr, R / 2, y, &sh.q_full);
+          for (int a = 0; a < 4; ++a) tma_load_2d(smem + a * K::QBOX, &tmQ, 64 * a, y, &sh.q_full);
+          if (!mbar_wait(&sh.q_full, c.kk & 1, abort_v, p.status)) break;
+        }
+        const int sls = g % NSL;
+        const uint32_t d = tbase + K::TM_S + sls * 2 * NH;
+        if (g >= NSL && !mbar_wait(&sh.s_free[sls], ((g / NSL) - 1) & 1, abort_v, p.status)) break;
+        if (!mbar_wait(&sh.r_full[rs], rph, abort_v, p.status)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          mma_f8(d, dr0 + (uint64_t)((rs * RBOX + k * 32) >> 4), dqr + (uint64_t)(k * 2),
+                 idesc_f8(2 * NH), k != 0);
+        mma_commit(&sh.r_empty[rs]);
+        if (++rs == NR) { rs = 0; rph ^= 1; }
+#pragma unroll 1
+        for (int a = 0; a < 4; ++a) {
+          if (!mbar_wait(&sh.c_full[slot], ph, abort_v, p.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t da = dc0 + (uint64_t)((slot * BOX) >> 4);
+          const uint64_t db = dq + (uint64_t)((a * K::QBOX) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f8(d, da + (uint64_t)(k * 2), db + (uint64_t)(k * 2), idesc_f8(2 * NH), 1);
+          if (++slot == NS) { slot = 0; ph ^= 1; }
+        }
+        if (!ok) break;
+        mma_commit(&sh.s_full[sls]);
+        if (c.j == c.s.nch - 1) mma_commit(&sh.q_free);
+        advance(c);
+      }
+    }
+  } else if (warp == 3) {
+    // ---------------- PV of every chunk
+    if (elect_one()) {
+      int slot = 0, g = 0;
+      const uint64_t dc0 = desc_mnmajor_sw128(smem_u32(smem + K::OFF_C), BOX);
+      const uint64_t dp0 = desc_mn<K::PW>(smem_u32(smem + K::OFF_P));
+      const uint64_t dsf = desc_sf(smem_u32(sh.sf[0]));
+      for (; !c.done; ++g) {
+        const int pb = g % NP;
+        if (c.j == 0 && c.kk > 0 && !mbar_wait(&sh.o_free, (c.kk - 1) & 1, abort_v, p.status))
+          break;
+        if (!mbar_wait(&sh.p_full[pb], (g / NP) & 1, abort_v, p.status)) break;
+        tc_fence_after();
+        const uint32_t sfb = tbase + K::TM_SFB + 4 * pb;
+        tmem_cp_sf(sfb, dsf + (uint64_t)((pb * 512) >> 4));
+        const uint64_t dp = dp0 + (uint64_t)((pb * K::PBYTES) >> 4);
+        const uint32_t keep = c.j != 0;
+#pragma unroll 1
+        for (int a = 0; a < 4; ++a) {
+          const uint64_t dc = dc0 + (uint64_t)((slot * BOX) >> 4);
+#pragma unroll
+          for (int term = 0; term < (K::STK ? 1 : 2); ++term)
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb)
+              mma_mxf8(tbase + K::TM_O + a * K::PN, dc + (uint64_t)((kb * 32 * 128) >> 4),
+                       dp + (uint64_t)((term * CT * 64 + kb * 32 * K::PW) >> 4),
+                       idesc_mxf8(K::PN, kb), tbase + K::TM_SFA, sfb,
+                       term || kb ? 1u : keep);
+          mma_commit(&sh.c_empty[slot]);
+          if (++slot == NS) slot = 0;
+        }
+        mma_commit(&sh.pv_done[pb]);
+        if (c.j == c.s.nch - 1) mma_commit(&sh.o_done);
+        advance(c);
+      }
+    }
+  } else if (warp == 2) {
+    // ---------------- lookups, and TMA of the last two boxes.  Lane i <
+    // 128 / bs looks up block i of a chunk, AHEAD chunks before its loads; the
+    // id of one chunk is loaded while the scale of the one before is.
     const int per_chunk = CT / p.bs;
     Cursor look = c;
-    constexpr int kNone = -1;                 // no block (kNone also for ids that are refused)
+    int ln = 0, n = 0, lg = 0;
     auto fetch = [&]() -> int {               // the id as the table has it; INT_MIN: no block
       int id = INT32_MIN;
       if (!look.done) {
+        if (look.j == 0) ln = p.len[look.s.b];
         const int t = (look.s.c0 + look.j) * CT + lane * p.bs;
-        if (lane < per_chunk && t < p.len[look.s.b]) {
+        if (lane < per_chunk && t < ln) {
           id = p.table[(int64_t)look.s.b * p.max_blocks + (t >> p.lbs)];
           if (id == INT32_MIN) id = -1;
         }
-        advance(look);
       }
       return id;
     };
-    auto check = [&](int id) -> int {         // a valid id, kNone without a block
-      if (id == INT32_MIN) return kNone;
-      if (id < 0 || id >= p.n_blocks) {
+    int id = fetch();
+    // Entry lg % GR was chunk lg - GR's = g - 3 of the chunk g just loaded,
+    // whose last box has waited for a box of chunk g - 2 (the ring holds less
+    // than three chunks): every softmax warp is past g - 3.
+    // Every load is used one call later, so that no call waits for one.
+    float sc = 1.f;                           // the scale of entry lg - 1
+    bool pending = false;
+    auto look_up = [&]() {
+      if (pending) {
+        const int at = (lg - 1) % GR;
+        int e;
+        if (!stored_exp(sc, &e)) {
+          atomicOr(p.status, kStatusBadPage);
+          sc = 1.f;
+        }
+        if (lane < 8) sh.scl[at][lane] = sc;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.e_full[at]);
+      }
+      pending = !look.done;
+      if (!pending) return;
+      const int at = lg % GR;
+      const bool has = id != INT32_MIN;
+      if (has && (id < 0 || id >= p.n_blocks)) {
         atomicOr(p.status, kStatusBadPage);
         id = 0;
       }
-      // the head groups of a unit share the prefetch
-      if (lane % p.groups == hg)
-        bulk_prefetch_l2(p.cache + (int64_t)id * p.bs * W, (uint32_t)(p.bs * W));
-      return id;
+      if (lane < 8) sh.ids[at][lane] = has ? id : 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.g_full[at]);
+      sc = 1.f;
+      if (has) {
+        sc = p.scales[id];
+        // the head groups of a unit share the prefetch
+        if (lg > 0 && lane % p.groups == hg)
+          bulk_prefetch_l2(p.cache + (int64_t)id * p.bs * W, (uint32_t)(p.bs * W));
+      }
+      advance(look);
+      id = fetch();
+      ++lg;
     };
-    auto scale_of = [&](int id) -> float { return id == kNone ? 1.f : p.scales[id]; };
-    int ids[PF + 1], raw;
-    float scs[PF + 1];
-    {
-      int first[PF + 2];
-#pragma unroll
-      for (int i = 0; i < PF + 2; ++i) first[i] = fetch();
-#pragma unroll
-      for (int i = 0; i < PF + 1; ++i) ids[i] = check(first[i]);
-#pragma unroll
-      for (int i = 0; i < PF + 1; ++i) scs[i] = scale_of(ids[i]);
-      raw = first[PF + 1];
-    }
-    int tails = 0, g = 0, fills = 0;
-    bool ok = true;
-    for (; !c.done; ++g) {
-      const int n = p.len[c.s.b], valid = min(CT, n - (c.s.c0 + c.j) * CT);
-      const int blocks = (valid + p.bs - 1) >> p.lbs, rows = blocks << p.lbs;
-      const bool tail = valid < CT;
-      const int id = ids[0], y = id << p.lbs;
-      // rope first: the scores start with it
-      const int rs = g % NR;
-      if (!warp_wait(&sh.r_empty[rs], ((g / NR) & 1) ^ 1, abort_v, p.status)) { ok = false; break; }
-      if (lane == 0) mbar_arrive_expect_tx(&sh.r_full[rs], rows * DR);
-      __syncwarp();
-      if (lane < blocks)
-        tma_load_2d(smem + K::OFF_R + rs * RBOX + (lane << p.lbs) * DR, &tmCr, R / 2, y,
-                    &sh.r_full[rs]);
-#pragma unroll 1
-      for (int a = 0; a < 4; ++a) {
-        const int f = 4 * g + a, slot = f % NS;
-        if (!warp_wait(&sh.c_empty[slot], ((f / NS) & 1) ^ 1, abort_v, p.status)) { ok = false; break; }
-        if (a == 0) {
-          // the ring has passed chunk g - 4, whose scales lay here
-          float s = scs[0];
-          int e;
-          if (!stored_exp(s, &e)) {
-            atomicOr(p.status, kStatusBadPage);
-            s = 1.f;
-          }
-          if (lane < 8) sh.scl[g & 3][lane] = s;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.g_full[g & 3]);
-        }
-        // a chunk that ends before its last row goes by way of warp 2
-        uint64_t* bar = tail ? &sh.t_full[tails & 3] : &sh.c_full[slot];
-        if (lane == 0) {
-          if (!tail) mbar_arrive_expect_tx(bar, rows * 128);
-          else if (a == 0) mbar_arrive_expect_tx(bar, 4 * rows * 128);
-        }
-        __syncwarp();
-        if (lane < blocks)
-          tma_load_2d(smem + K::OFF_C + slot * BOX + (lane << p.lbs) * 128, &tmC, 64 * a, y, bar);
-        fills = f + 1;
-      }
-      if (!ok) break;
-      if (tail) ++tails;
-      advance(c);
-#pragma unroll
-      for (int i = 0; i < PF; ++i) {
-        ids[i] = ids[i + 1];
-        scs[i] = scs[i + 1];
-      }
-      ids[PF] = check(raw);
-      scs[PF] = scale_of(ids[PF]);
-      raw = fetch();
-    }
-    if (!ok && lane == 0) {                   // copies in flight land before the block ends
-      int given_up = 0;
-      for (int f = max(0, fills - NS); f < fills; ++f)
-        mbar_wait(&sh.c_full[f % NS], (f / NS) & 1, &given_up, nullptr);
-    }
-  } else if (warp == 2) {
-    // ---------------- the segment's query; zeros behind the last token
-    int g0 = 0, tails = 0;
-    for (; !c.done; c.next_seg(p.pre, p.B, sl, u)) {
-      if (c.kk > 0 && !warp_wait(&sh.q_free, (c.kk - 1) & 1, abort_v, p.status)) break;
+    look_up();
+    int slot = 2;
+    uint32_t ph = 1;
+    for (int g = 0; !c.done; ++g) {
+      bool ok = true;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&sh.q_full, K::QBYTES);
-        const int y = (c.s.b * p.groups + hg) * 2 * NH;
-        tma_load_2d(smem + 4 * K::QBOX, &tmQr, R / 2, y, &sh.q_full);
-        for (int a = 0; a < 4; ++a) tma_load_2d(smem + a * K::QBOX, &tmQ, 64 * a, y, &sh.q_full);
-      }
-      __syncwarp();
-      const int valid = min(CT, p.len[c.s.b] - (c.s.c0 + c.s.nch - 1) * CT);
-      g0 += c.s.nch;
-      if (valid < CT) {
-        if (!warp_wait(&sh.t_full[tails & 3], (tails >> 2) & 1, abort_v, p.status)) break;
-        ++tails;
+        if (c.j == 0) n = p.len[c.s.b];
+        const int valid = min(CT, n - (c.s.c0 + c.j) * CT);
+        const int blocks = (valid + p.bs - 1) >> p.lbs;
 #pragma unroll 1
-        for (int a = 0; a < 4; ++a) {
-          const uint32_t box = smem_u32(smem + K::OFF_C + ((4 * (g0 - 1) + a) % NS) * BOX);
-          for (int i = valid * 8 + lane; i < CT * 8; i += 32) st_shared_v4(box + i * 16, 0, 0, 0, 0);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0)
-          for (int a = 0; a < 4; ++a) mbar_arrive(&sh.c_full[(4 * (g0 - 1) + a) % NS]);
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------- MMA issue: whichever of S of chunk gs (in five steps, as
-    // its boxes arrive) and PV of chunk gp is ready, PV first (it frees boxes)
-    if (elect_one()) {
-      Cursor cs = c, cp = c;
-      int gs = 0, step = 0, gp = 0;
-      uint64_t t_stall = 0;
-      uint32_t idle = 0;
-      const uint32_t q_base = smem_u32(smem), c_base = smem_u32(smem + K::OFF_C);
-      while (!cp.done) {
-        bool progress = false;
-        if (gp < gs && mbar_test(&sh.p_full[gp % NP], (gp / NP) & 1) &&
-            (cp.j != 0 || cp.kk == 0 || mbar_test(&sh.o_free, (cp.kk - 1) & 1))) {
-          tc_fence_after();
-          const int pb = gp % NP;
-          const uint32_t sfb = tbase + K::TM_SFB + 4 * pb;
-          tmem_cp_sf(sfb, desc_sf(smem_u32(sh.sf[pb])));
-          const uint64_t dp = desc_mn<K::PW>(smem_u32(smem + K::OFF_P + pb * K::PBYTES));
-#pragma unroll 1
-          for (int a = 0; a < 4; ++a) {
-            const int slot = (4 * gp + a) % NS;
-            const uint64_t dc = desc_mnmajor_sw128(c_base + slot * BOX, BOX);
-#pragma unroll
-            for (int term = 0; term < (K::STK ? 1 : 2); ++term)
-#pragma unroll
-              for (int kb = 0; kb < 4; ++kb)
-                mma_mxf8(tbase + K::TM_O + a * K::PN, dc + (uint64_t)((kb * 32 * 128) >> 4),
-                         dp + (uint64_t)((term * CT * 64 + kb * 32 * K::PW) >> 4),
-                         idesc_mxf8(K::PN, kb), tbase + K::TM_SFA, sfb,
-                         (cp.j | term | kb) != 0);
-            mma_commit(&sh.c_empty[slot]);
-          }
-          mma_commit(&sh.pv_done[pb]);
-          if (cp.j == cp.s.nch - 1) mma_commit(&sh.o_done);
-          ++gp;
-          advance(cp);
-          progress = true;
-        }
-        if (!cs.done) {
-          const uint32_t d = tbase + K::TM_S + (gs % NSL) * 2 * NH;
-          if (step == 0) {
-            if ((cs.j != 0 || mbar_test(&sh.q_full, cs.kk & 1)) &&
-                (gs < NSL || mbar_test(&sh.s_free[gs % NSL], ((gs / NSL) - 1) & 1)) &&
-                mbar_test(&sh.r_full[gs % NR], (gs / NR) & 1)) {
-              tc_fence_after();
-              const uint64_t da = desc_kmajor_sw64(smem_u32(smem + K::OFF_R + (gs % NR) * RBOX));
-              const uint64_t db = desc_kmajor_sw64(q_base + 4 * K::QBOX);
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                mma_f8(d, da + (uint64_t)(k * 2), db + (uint64_t)(k * 2), idesc_f8(2 * NH), k != 0);
-              mma_commit(&sh.r_empty[gs % NR]);
-              step = 1;
-              progress = true;
-            }
-          } else {
-            const int f = 4 * gs + step - 1, slot = f % NS;
-            if (mbar_test(&sh.c_full[slot], (f / NS) & 1)) {
-              tc_fence_after();
-              const uint64_t da = desc_kmajor_sw128(c_base + slot * BOX);
-              const uint64_t db = desc_kmajor_sw128(q_base + (step - 1) * K::QBOX);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f8(d, da + (uint64_t)(k * 2), db + (uint64_t)(k * 2), idesc_f8(2 * NH), 1);
-              if (step == 4) {
-                mma_commit(&sh.s_full[gs % NSL]);
-                if (cs.j == cs.s.nch - 1) mma_commit(&sh.q_free);
-                ++gs;
-                advance(cs);
-                step = 0;
-              } else {
-                ++step;
-              }
-              progress = true;
-            }
-          }
-        }
-        if (progress) {
-          idle = 0;
-        } else if ((++idle & 63u) == 0) {     // bounded like every other wait
-          const uint64_t now = globaltimer();
-          if (idle == 64) t_stall = now;
-          if (*abort_v) break;
-          if (now - t_stall > kWaitNs) {
-            *abort_v = 1;
-            atomicOr(p.status, kStatusTimeout);
-            break;
-          }
+        for (int a = 2; ok && a < 4; ++a) {
+          ok = mbar_wait(&sh.c_empty[slot], ph, abort_v, p.status);
+          if (!ok) break;
+          load_box(a, slot, blocks, sh.ids[g % GR]);
+          slot += a == 2 ? 1 : 3;
+          if (slot >= NS) { slot -= NS; ph ^= 1; }
         }
       }
+      if (!__shfl_sync(0xffffffffu, (int)ok, 0)) break;
+      while (lg <= g + AHEAD && (pending || !look.done)) look_up();
+      advance(c);
     }
-  } else if (warp >= 4) {
-    // ---------------- softmax: thread = token, group = half of the heads
+    if (lane == 0 && *abort_v) drain(slot, ph);
+  } else {
+    // ---------------- softmax: thread = token, group = HPG heads
     const int grp = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
     const int h0 = grp * HPG, bar = 1 + grp;
     const int tg = (int)threadIdx.x - 128 - 128 * grp;
@@ -648,68 +688,110 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t p_base = smem_u32(smem + K::OFF_P);
     const int head0 = hg * p.hg_heads + h0;   // this group's first head
     const int n_heads = max(0, min(min(HPG, p.hg_heads - h0), p.h - head0));   // real ones
+    float* const inv_w = sh.inv[grp][quad];   // this warp's 2^-k per head
     bool ok = true;
     int g = 0;
     for (; !c.done; c.next_seg(p.pre, p.B, sl, u)) {
       const Seg s = c.s;
       const int n = p.len[s.b];
-      if (tg < HPG) sh.hf[h0 + tg] = p.qf[((int64_t)s.b * p.groups + hg) * NH + h0 + tg];
+      if (tg < HPG) {
+        sh.hf[h0 + tg] = p.qf[((int64_t)s.b * p.groups + hg) * NH + h0 + tg];
+        sh.nref[h0 + tg] = 0.f;               // the first chunk sets it
+      }
       named_barrier_sync(bar, 128);
       float l[HPG];
 #pragma unroll
       for (int i = 0; i < HPG; ++i) l[i] = 0.f;
       for (int j = 0; j < s.nch; ++j, ++g) {
         const int sls = g % NSL, pb = g % NP;
-        ok = ok && warp_wait(&sh.s_full[sls], (g / NSL) & 1, abort_v, p.status) &&
-             warp_wait(&sh.g_full[g & 3], (g >> 2) & 1, abort_v, p.status);
-        const float sc = sh.scl[g & 3][row >> p.lbs];
         const bool live = row < n - (s.c0 + j) * CT;
-        float v[HPG], us[HPG];
+        ok = ok && warp_wait(&sh.e_full[g % GR], (g / GR) & 1, abort_v, p.status);
+        const float sc = sh.scl[g % GR][row >> p.lbs];
+        ok = ok && warp_wait(&sh.s_full[sls], (g / NSL) & 1, abort_v, p.status);
+        float v[HPG], pr[HPG], vm = -INFINITY;
         {
           uint32_t a[HPG], b[HPG];
           tc_fence_after();
           const uint32_t ts = tbase + lane_off + K::TM_S + sls * 2 * NH + h0;
-#pragma unroll
-          for (int i = 0; i < HPG; i += 8) {
-            tmem_ld8(ts + i, a + i);
-            tmem_ld8(ts + NH + i, b + i);
-          }
+          tmem_ld_n<HPG>(ts, a);
+          tmem_ld_n<HPG>(ts + NH, b);
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.s_free[sls]);
-          // raw scores of the block's values
+          // v = raw 2^e f - ref
 #pragma unroll
-          for (int i = 0; i < HPG; ++i)
-            us[i] = (__uint_as_float(a[i]) + __uint_as_float(b[i])) * sc;
-        }
-        bool need = j == 0;
-        if (j > 0) {
-          float vm = -INFINITY;
+          for (int i = 0; i < HPG; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&sh.hf[h0 + i]);
+            const float4 r = *reinterpret_cast<const float4*>(&sh.nref[h0 + i]);
+            const float ff[4] = {f.x, f.y, f.z, f.w}, rr[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-          for (int i = 0; i < HPG; ++i) {
-            v[i] = fmaf(us[i], sh.hf[h0 + i], -sh.ref[h0 + i]);
-            vm = fmaxf(vm, v[i]);
+            for (int k = 0; k < 4; k += 2) {
+              float x = __uint_as_float(a[i + k]), y = __uint_as_float(a[i + k + 1]);
+              add2(x, y, __uint_as_float(b[i + k]), __uint_as_float(b[i + k + 1]));
+              mul2(x, y, sc, sc);
+              fma2(v[i + k], v[i + k + 1], x, y, ff[k], ff[k + 1], rr[k], rr[k + 1]);
+              vm = max3f(vm, v[i + k], v[i + k + 1]);
+            }
           }
-          need = live && vm > kGrow;
         }
-        if (barrier_or(bar, 128, need || !ok)) {
-          // first chunk of the segment, or a score far above its reference
-          if (barrier_or(bar, 128, !ok)) { ok = false; break; }
+        if (!live) {                          // behind the last token
+#pragma unroll
+          for (int i = 0; i < HPG; ++i) v[i] = -INFINITY;
+        }
+        // the rare case: the segment's first chunk, or a score far above its
+        // reference (or a warp that gave up)
+        const bool far = barrier_or(bar, 128, j == 0 || !ok || (live && vm > kGrow));
+        uint32_t m[HPG / 2];
+        int pair;                             // of heads whose maximum this lane ends with
+        bool leave = false;
+        for (bool checked = false;;) {
+#pragma unroll
+          for (int i = 0; i < HPG; ++i) pr[i] = ex2(v[i]);
+          // The largest p 2^e of the warp's 32 tokens per head, from the upper
+          // halves of the (non-negative) floats, whose order is that of their
+          // bits, NaN above all: lanes trade halves of their heads until a lane
+          // has two.
+#pragma unroll
+          for (int i = 0; i < HPG / 2; ++i) {
+            float x = pr[2 * i], y = pr[2 * i + 1];
+            mul2(x, y, sc, sc);
+            m[i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+          }
+          pair = 0;
+#pragma unroll
+          for (int w = HPG / 4, o = 16; o; w >>= 1, o >>= 1) {
+            if (w > 0) {
+              const bool up = lane & o;
+              pair = 2 * pair + up;
+#pragma unroll
+              for (int i = 0; i < w; ++i) {
+                const uint32_t give = up ? m[i] : m[i + w], mine = up ? m[i + w] : m[i];
+                m[i] = max_u16x2(mine, __shfl_xor_sync(0xffffffffu, give, o));
+              }
+            } else {
+              m[0] = max_u16x2(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+            }
+          }
+          if (checked) break;
+          checked = true;
+          if (!far) break;
+          // new references; if a warp gave up, the group leaves together
+          if (barrier_or(bar, 128, !ok)) { leave = true; break; }
           int mine = 0;
 #pragma unroll
           for (int i = 0; i < HPG; ++i) {
-            const int k = __reduce_max_sync(
-                0xffffffffu, float_key(live ? us[i] * sh.hf[h0 + i] : -INFINITY));
+            v[i] -= sh.nref[h0 + i];          // the score itself
+            const int k = __reduce_max_sync(0xffffffffu, float_key(v[i]));
             if (lane == i) mine = k;
           }
           if (lane < HPG) sh.hmax[grp][quad][lane] = mine;
           named_barrier_sync(bar, 128);
           if (quad == 0 && lane < HPG) {
-            const float m = key_float(max(max(sh.hmax[grp][0][lane], sh.hmax[grp][1][lane]),
+            const float x = key_float(max(max(sh.hmax[grp][0][lane], sh.hmax[grp][1][lane]),
                                           max(sh.hmax[grp][2][lane], sh.hmax[grp][3][lane])));
-            const float old = j == 0 ? m : sh.ref[h0 + lane], now = m > old ? m : old;
-            sh.ref[h0 + lane] = now;
+            const float old = j == 0 ? x : -sh.nref[h0 + lane], now = x > old ? x : old;
+            sh.nref[h0 + lane] = -now;
             sh.alpha[h0 + lane] = ex2(old - now);
           }
           named_barrier_sync(bar, 128);
@@ -738,45 +820,58 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tmem_wait_st();
           }
 #pragma unroll
-          for (int i = 0; i < HPG; ++i) v[i] = fmaf(us[i], sh.hf[h0 + i], -sh.ref[h0 + i]);
+          for (int i = 0; i < HPG; ++i) v[i] += sh.nref[h0 + i];
         }
-        // p, its row sums, and p 2^e with a power of two per 32 tokens
-        uint32_t hi[HPG / 4], lo[HPG / 4], sfb = 0;
-#pragma unroll
-        for (int i = 0; i < HPG; i += 4) {
-          float w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float pr = live ? ex2(v[i + k]) : 0.f;
-            l[i + k] += pr;
-            w[k] = pr * sc;
-            // the largest of the 32 (positive floats in the order of their
-            // bits, NaN above all) goes to [128, 256)
-            const uint32_t m = max(__reduce_max_sync(0xffffffffu, __float_as_uint(w[k])), 8u << 23);
-            const uint32_t ex = m & 0x7f800000u;
-            w[k] *= __uint_as_float(0x82800000u - ex);
-            if (lane == i + k) sfb = (ex >> 23) - 7;
-          }
-          const uint32_t w01 = pack_f16(w[0], w[1]), w23 = pack_f16(w[2], w[3]);
-          const uint32_t h01 = f16x2_to_e4m3x2(w01), h23 = f16x2_to_e4m3x2(w23);
-          hi[i / 4] = h01 | (h23 << 16);
-          lo[i / 4] = f16x2_to_e4m3x2(sub_f16x2(w01, e4m3x2_to_f16x2(h01))) |
-                      (f16x2_to_e4m3x2(sub_f16x2(w23, e4m3x2_to_f16x2(h23))) << 16);
-        }
-        // PV of chunk g - NP has run: this buffer is free
+        if (leave) { ok = false; break; }
+        // PV of chunk g - NP has run: this P buffer and its scales are free
         if (g >= NP) ok = ok && warp_wait(&sh.pv_done[pb], ((g / NP) - 1) & 1, abort_v, p.status);
-        const uint32_t pt = p_base + pb * K::PBYTES;
-        const uint32_t lo_at = K::STK ? NH : 0, lo_tile = K::STK ? 0 : CT * 64;
+        // the largest goes to [128, 256): factor 2^-k, and the scale 2^k as a
+        // ue8m0 byte
+        constexpr int SAME = 64 / HPG;        // lanes with the same pair
+        if (lane % SAME == 0) {
 #pragma unroll
-        for (int i = 0; i < HPG / 4; i += 2) {
-          const uint32_t at = row * K::PW + h0 + 4 * i;
-          st_shared_v2(pt + swz<K::PW>(at), hi[i], hi[i + 1]);
-          st_shared_v2(pt + lo_tile + swz<K::PW>(at + lo_at), lo[i], lo[i + 1]);
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t ex = max((k ? m[0] >> 16 : m[0] & 0xffffu) & 0x7f80u, 8u << 7) << 16;
+            inv_w[2 * pair + k] = __uint_as_float(0x82800000u - ex);
+            const int nh = h0 + 2 * pair + k;
+            const uint8_t sfb = (uint8_t)((ex >> 23) - 7);
+            sh.sf[pb][(nh & 31) * 16 + (nh >> 5) * 4 + quad] = sfb;
+            if (K::STK) sh.sf[pb][((nh + NH) & 31) * 16 + ((nh + NH) >> 5) * 4 + quad] = sfb;
+          }
         }
-        if (lane < HPG) {
-          const int nh = h0 + lane;
-          sh.sf[pb][(nh & 31) * 16 + (nh >> 5) * 4 + quad] = (uint8_t)sfb;
-          if (K::STK) sh.sf[pb][((nh + NH) & 31) * 16 + ((nh + NH) >> 5) * 4 + quad] = (uint8_t)sfb;
+        __syncwarp();
+        const uint32_t pt = p_base + pb * K::PBYTES;
+        constexpr uint32_t lo_at = K::STK ? NH : 0, lo_tile = K::STK ? 0 : CT * 64;
+#pragma unroll
+        for (int i = 0; i < HPG; i += 8) {
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float4 f = *reinterpret_cast<const float4*>(inv_w + i + 4 * q);
+            mul2(f.x, f.y, sc, sc);
+            mul2(f.z, f.w, sc, sc);
+            float* const w = pr + i + 4 * q;
+            add2(l[i + 4 * q], l[i + 4 * q + 1], w[0], w[1]);
+            add2(l[i + 4 * q + 2], l[i + 4 * q + 3], w[2], w[3]);
+            mul2(w[0], w[1], f.x, f.y);
+            mul2(w[2], w[3], f.z, f.w);
+            const uint32_t w01 = pack_f16(w[0], w[1]), w23 = pack_f16(w[2], w[3]);
+            const uint32_t h01 = f16x2_to_e4m3x2(w01), h23 = f16x2_to_e4m3x2(w23);
+            hi[q] = h01 | (h23 << 16);
+            lo[q] = f16x2_to_e4m3x2(sub_f16x2(w01, e4m3x2_to_f16x2(h01))) |
+                    (f16x2_to_e4m3x2(sub_f16x2(w23, e4m3x2_to_f16x2(h23))) << 16);
+          }
+          const uint32_t at = row * K::PW + h0 + i;
+          st_shared_v2(pt + swz<K::PW>(at), hi[0], hi[1]);
+          st_shared_v2(pt + lo_tile + swz<K::PW>(at + lo_at), lo[0], lo[1]);
+        }
+        // a weight of 0 times whatever lies behind the last token could be NaN
+        if (!live) {
+          for (int i = grp; i < 32; i += NG) {
+            const int slot = (4 * g + (i >> 3)) % NS;
+            st_shared_v4(smem_u32(smem + K::OFF_C + slot * BOX) + row * 128 + (i & 7) * 16, 0, 0, 0,
+                         0);
+          }
         }
         fence_proxy_async();
         tc_fence_before();                    // a rescaled O comes before this PV
@@ -797,46 +892,41 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (lane < HPG) sh.lsum[grp][quad][lane] = mine;
       }
       named_barrier_sync(bar, 128);
+      if (lane < HPG) {
+        const float sum = (sh.lsum[grp][0][lane] + sh.lsum[grp][1][lane]) +
+                          (sh.lsum[grp][2][lane] + sh.lsum[grp][3][lane]);
+        sh.alpha[h0 + lane] = 1.f / sum;        // the same from all four warps
+        if (!s.whole && quad == 0 && lane < n_heads)
+          p.part_lse[(int64_t)s.slot * p.h + head0 + lane] = log2f(sum) - sh.nref[h0 + lane];
+      }
+      __syncwarp();
       ok = warp_wait(&sh.o_done, c.kk & 1, abort_v, p.status);
       tc_fence_after();
       if (ok) {
-        const auto sum_of = [&](int i) {
-          return (sh.lsum[grp][0][i] + sh.lsum[grp][1][i]) +
-                 (sh.lsum[grp][2][i] + sh.lsum[grp][3][i]);
-        };
 #pragma unroll 1
-        for (int i = 0; i < HPG; i += 8) {
-          float inv[8];
+        for (int a = 0; a < 4; ++a) {
+          uint32_t o[HPG], o2[HPG];
+          const uint32_t to = tbase + lane_off + K::TM_O + a * K::PN + h0;
+          tmem_ld_n<HPG>(to, o);
+          if (K::STK) tmem_ld_n<HPG>(to + NH, o2);
+          tmem_wait_ld();
+          if (a == 3) {
+            tc_fence_before();                // O may be overwritten
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_free);
+          }
+          const int dim = a * 128 + row;
+          __nv_bfloat16* dl = p.o_lat + ((int64_t)s.b * p.h + head0) * R + dim;
+          float* dp = p.part_o + ((int64_t)s.slot * p.h + head0) * R + dim;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) inv[k] = 1.f / sum_of(i + k);
-#pragma unroll 1
-          for (int a = 0; a < 4; ++a) {
-            uint32_t o[8], o2[8];
-            const uint32_t to = tbase + lane_off + K::TM_O + a * K::PN + h0 + i;
-            tmem_ld8(to, o);
-            if (K::STK) tmem_ld8(to + NH, o2);
-            tmem_wait_ld();
-            const int dim = a * 128 + row;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (i + k >= n_heads) continue;
-              float x = __uint_as_float(o[k]);
-              if (K::STK) x += __uint_as_float(o2[k]);
-              x *= inv[k];
-              const int head = head0 + i + k;
-              if (s.whole)
-                p.o_lat[((int64_t)s.b * p.h + head) * R + dim] = __float2bfloat16(x);
-              else
-                p.part_o[((int64_t)s.slot * p.h + head) * R + dim] = x;
-            }
+          for (int k = 0; k < HPG; ++k) {
+            if (k >= n_heads) continue;
+            float x = __uint_as_float(o[k]);
+            if (K::STK) x += __uint_as_float(o2[k]);
+            x *= sh.alpha[h0 + k];
+            if (s.whole) dl[k * R] = __float2bfloat16(x); else dp[k * R] = x;
           }
         }
-        if (!s.whole && quad == 0 && lane < n_heads)
-          p.part_lse[(int64_t)s.slot * p.h + head0 + lane] =
-              sh.ref[h0 + lane] + log2f(sum_of(lane));
-        tc_fence_before();                    // O may be overwritten
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.o_free);
       }
     }
   }
@@ -893,7 +983,7 @@ cudaError_t launch_attn(const AttnParams& p, const CUtensorMap& tmQ, const CUten
   static std::atomic<uint64_t> set{0};
   const cudaError_t e = set_dynamic_smem((const void*)paged_attn_kernel<NH>, smem_bytes<NH>(), set);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_attn_kernel<NH>, dim3(p.n_units * p.groups), dim3(NTHREADS),
+  return launch_pdl(paged_attn_kernel<NH>, dim3(p.n_units * p.groups), dim3(Cfg<NH>::NTHREADS),
                     smem_bytes<NH>(), st, tmQ, tmQr, tmC, tmCr, p);
 }
 

@@ -86,10 +86,11 @@ struct Cursor {
       ++b;
     }
   }
-  MLA_PHD void start(const int64_t* pre, int B, const Slice& sl, int u) {
+  // b: the sequence at the slice's start, seq_at(pre, B, sl.r0)
+  MLA_PHD void start(const int64_t* pre, int B, const Slice& sl, int u, int b) {
     kk = 0; j = 0;
     if (sl.r0 >= sl.r1) { done = true; return; }
-    seek(pre, B, sl, u, seq_at(pre, B, sl.r0));
+    seek(pre, B, sl, u, b);
   }
   MLA_PHD void next_seg(const int64_t* pre, int B, const Slice& sl, int u) {
     j = 0; ++kk;

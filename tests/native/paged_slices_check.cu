@@ -43,7 +43,7 @@ int main() {
     for (int u = 0; u < units; ++u) {
       const Slice sl = unit_slice(pre.data(), B, u, units, min_len);
       Cursor k;
-      k.start(pre.data(), B, sl, u);
+      k.start(pre.data(), B, sl, u, seq_at(pre.data(), B, sl.r0));
       int last = -1, kk = 0;
       while (!k.done) {
         const Seg s = k.s;
