@@ -475,7 +475,7 @@ MLA_API mla_status mla_paged_gather(const mla_config* cfg, const void* cache, co
  * tensor cores (the shapes of mla_decode_absorbed's) split_tokens is the
  * granule in which sequences are cut and max_splits the number of partial
  * slots, which depends on the current device's SM count; q8 and plan are -1 on
- * CUDA cores. */
+ * CUDA cores, q_lat on tensor cores, where o_lat is fp32. */
 typedef struct mla_paged_layout {
   int64_t status, q_lat, q8, plan, part_o, part_lse, o_lat, o, total_bytes;
   int32_t split_tokens, max_splits;

@@ -282,6 +282,66 @@ def mla_decode_absorbed_noalloc(cfg, q_nope, q_pe, w_kv_b, latent_cache, cu_ctx,
 
 
 # ------------------------------------------------- the paged 8-bit cache
+# A serving step makes several of these calls, some of a few microseconds, so
+# their checks are one pass over the tensors: _ptr is asked for the words only
+# when something is wrong.
+def _torch():
+    global _T, _I32, _F32, _FP8, _U8, _DTYPES, _raw_stream
+    import torch
+    _T, _I32, _F32 = torch, torch.int32, torch.float32
+    _FP8, _U8 = torch.float8_e4m3fn, torch.uint8
+    _DTYPES = {MLA_BF16: torch.bfloat16, MLA_F32: torch.float32}
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch
+
+
+_T = None
+
+
+def _ptrs(workspace, tensors):
+    """Device pointers of ``tensors``, (tensor, name, dtype, elements, optional)
+    each, after the checks of ``_ptr``, and that all lie on the workspace's
+    device, which has to be the current one (the kernels launch there)."""
+    dev = workspace.device if workspace is not None else None
+    out = []
+    for t, name, dtype, numel, optional in tensors:
+        if t is None:
+            if not optional:
+                raise ValueError(f"{name} is required")
+            out.append(None)
+            continue
+        if (t.dtype is not dtype or t.numel() < numel or not t.is_cuda
+                or not t.is_contiguous()):
+            _ptr(t, name, optional, dtype, numel)
+        if t.device != dev and dev is not None:
+            raise ValueError(f"tensors on different devices: {name} on {t.device}, workspace "
+                             f"on {dev}")
+        out.append(t.data_ptr())
+    if workspace is None or not workspace.is_cuda or not workspace.is_contiguous():
+        _ptr(workspace, "workspace")
+    if dev.type == "cuda" and dev.index != _T.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, but the current device is "
+                         f"cuda:{_T.cuda.current_device()}")
+    out.append(workspace.data_ptr())
+    out.append(workspace.numel() * workspace.element_size())
+    return out
+
+
+def _stream_of(stream, workspace):
+    if stream is None:
+        if _raw_stream is None:
+            return _T.cuda.current_stream().cuda_stream
+        return _raw_stream(workspace.device.index)
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _pool(c, cache, scales, n_blocks, block_size):
+    """Checks of the pool's blocks (e4m3, or their bytes as uint8) and scales."""
+    dt = _U8 if cache is not None and cache.dtype is _U8 else _FP8
+    n = n_blocks * block_size * (c.kv_lora_rank + c.qk_rope_head_dim)
+    return (cache, "cache", dt, n, False), (scales, "scales", _F32, n_blocks, False)
+
+
 def mla_paged_workspace_size(n_blocks):
     n = _lib.load().mla_paged_workspace_size(int(n_blocks))
     if n == 0:
@@ -289,76 +349,63 @@ def mla_paged_workspace_size(n_blocks):
     return n
 
 
-def _ws(workspace, *tensors):
-    """The workspace pair, after checking that every tensor of the call lies on
-    the workspace's device and that this is the current one (the kernels launch
-    there)."""
-    import torch
-    p, dev = _ptr(workspace, "workspace"), workspace.device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {t.device} and workspace on {dev}")
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return p, C.c_size_t(workspace.numel() * workspace.element_size())
-
-
-def _pool_ptrs(c, cache, scales, n_blocks, block_size):
-    """The pool's blocks (e4m3, or their bytes as uint8) and scales."""
-    import torch
-    dt = torch.uint8 if cache is not None and cache.dtype == torch.uint8 else torch.float8_e4m3fn
-    n = int(n_blocks) * int(block_size) * (c.kv_lora_rank + c.qk_rope_head_dim)
-    return (_ptr(cache, "cache", False, dt, n),
-            _ptr(scales, "scales", False, _f32(), int(n_blocks)))
-
-
 def mla_paged_plan(ctx_len, new_len, block_table, free_ring, free_state, ctx_out, free_state_out,
                    slot_map, positions, cu_new, B, max_blocks, n_blocks, block_size, capacity,
                    workspace, stream=None):
     """Block tables and slot maps of one step (all int32 device tensors);
     ``positions`` may be None, and ``slot_map`` too when ``capacity`` is 0."""
-    i32, B, cap = _i32(), int(B), int(capacity)
-    _check(_lib.load().mla_paged_plan(
-        _ptr(ctx_len, "ctx_len", False, i32, B), _ptr(new_len, "new_len", False, i32, B),
-        _ptr(block_table, "block_table", False, i32, B * int(max_blocks)),
-        _ptr(free_ring, "free_ring", False, i32, int(n_blocks)),
-        _ptr(free_state, "free_state", False, i32, 2), _ptr(ctx_out, "ctx_out", False, i32, B),
-        _ptr(free_state_out, "free_state_out", False, i32, 2),
-        _ptr(slot_map, "slot_map", cap == 0, i32, cap),
-        _ptr(positions, "positions", True, i32, cap), _ptr(cu_new, "cu_new", False, i32, B + 1),
-        B, int(max_blocks), int(n_blocks), int(block_size), cap,
-        *_ws(workspace, ctx_len, new_len, block_table, free_ring, free_state, ctx_out,
-             free_state_out, slot_map, positions, cu_new), _stream(stream)))
+    if _T is None:
+        _torch()
+    *a, ws, size = _ptrs(workspace, (
+        (ctx_len, "ctx_len", _I32, B, False), (new_len, "new_len", _I32, B, False),
+        (block_table, "block_table", _I32, B * max_blocks, False),
+        (free_ring, "free_ring", _I32, n_blocks, False),
+        (free_state, "free_state", _I32, 2, False), (ctx_out, "ctx_out", _I32, B, False),
+        (free_state_out, "free_state_out", _I32, 2, False),
+        (slot_map, "slot_map", _I32, capacity, capacity == 0),
+        (positions, "positions", _I32, capacity, True), (cu_new, "cu_new", _I32, B + 1, False)))
+    status = _lib.load().mla_paged_plan(*a, B, max_blocks, n_blocks, block_size, capacity, ws,
+                                        size, _stream_of(stream, workspace))
+    if status:
+        _check(status)
 
 
 def mla_paged_append(cfg, rows, slot_map, cache, scales, n_rows, n_blocks, block_size, workspace,
                      stream=None):
     """Quantise ``rows`` [n_rows, kv_lora_rank + rope] into the slots of
     ``slot_map`` (-1: skip)."""
+    if _T is None:
+        _torch()
     c = cfg if isinstance(cfg, mla_config) else make_config(cfg)
-    n, row = int(n_rows), c.kv_lora_rank + c.qk_rope_head_dim
-    _check(_lib.load().mla_paged_append(
-        C.byref(c), _ptr(rows, "rows", False, _dt(c), n * row),
-        _ptr(slot_map, "slot_map", False, _i32(), n),
-        *_pool_ptrs(c, cache, scales, n_blocks, block_size), n, int(n_blocks), int(block_size),
-        *_ws(workspace, rows, slot_map, cache, scales), _stream(stream)))
+    row = c.kv_lora_rank + c.qk_rope_head_dim
+    *a, ws, size = _ptrs(workspace, (
+        (rows, "rows", _DTYPES.get(c.dtype), n_rows * row, False),
+        (slot_map, "slot_map", _I32, n_rows, False),
+        *_pool(c, cache, scales, n_blocks, block_size)))
+    status = _lib.load().mla_paged_append(C.byref(c), *a, n_rows, n_blocks, block_size, ws, size,
+                                          _stream_of(stream, workspace))
+    if status:
+        _check(status)
 
 
 def mla_paged_gather(cfg, cache, scales, block_table, ctx_len, rows_out, cu_ctx, B, max_blocks,
                      n_blocks, block_size, capacity, workspace, stream=None):
     """Rows of all requests back to back into ``rows_out`` [capacity, ...],
     their prefix sums into ``cu_ctx`` [B + 1]."""
+    if _T is None:
+        _torch()
     c = cfg if isinstance(cfg, mla_config) else make_config(cfg)
-    B, cap, row = int(B), int(capacity), c.kv_lora_rank + c.qk_rope_head_dim
-    _check(_lib.load().mla_paged_gather(
-        C.byref(c), *_pool_ptrs(c, cache, scales, n_blocks, block_size),
-        _ptr(block_table, "block_table", False, _i32(), B * int(max_blocks)),
-        _ptr(ctx_len, "ctx_len", False, _i32(), B),
-        _ptr(rows_out, "rows_out", cap == 0, _dt(c), cap * row),
-        _ptr(cu_ctx, "cu_ctx", False, _i32(), B + 1), B, int(max_blocks), int(n_blocks),
-        int(block_size), cap, *_ws(workspace, cache, scales, block_table, ctx_len, rows_out,
-                                   cu_ctx), _stream(stream)))
+    row = c.kv_lora_rank + c.qk_rope_head_dim
+    *a, ws, size = _ptrs(workspace, (
+        *_pool(c, cache, scales, n_blocks, block_size),
+        (block_table, "block_table", _I32, B * max_blocks, False),
+        (ctx_len, "ctx_len", _I32, B, False),
+        (rows_out, "rows_out", _DTYPES.get(c.dtype), capacity * row, capacity == 0),
+        (cu_ctx, "cu_ctx", _I32, B + 1, False)))
+    status = _lib.load().mla_paged_gather(C.byref(c), *a, B, max_blocks, n_blocks, block_size,
+                                          capacity, ws, size, _stream_of(stream, workspace))
+    if status:
+        _check(status)
 
 
 def mla_decode_paged_workspace_size(cfg, B, max_blocks, block_size):
@@ -374,17 +421,20 @@ def mla_decode_paged_workspace_size(cfg, B, max_blocks, block_size):
 def mla_decode_paged(cfg, q_nope, q_pe, w_kv_b, cache, scales, block_table, ctx_len, B,
                      max_blocks, n_blocks, block_size, w_o, out, workspace, stream=None):
     """One query token per request over the blocks of its table."""
+    if _T is None:
+        _torch()
     c = cfg if isinstance(cfg, mla_config) else make_config(cfg)
-    B, h, r, dt = int(B), c.num_heads, c.kv_lora_rank, _dt(c)
+    h, r, dt = c.num_heads, c.kv_lora_rank, _DTYPES.get(c.dtype)
     dn, dr, dv, H = c.qk_nope_head_dim, c.qk_rope_head_dim, c.v_head_dim, c.hidden_size
-    _check(_lib.load().mla_decode_paged(
-        C.byref(c), _ptr(q_nope, "q_nope", False, dt, B * h * dn),
-        _ptr(q_pe, "q_pe", False, dt, B * h * dr),
-        _ptr(w_kv_b, "w_kv_b", False, dt, h * (dn + dv) * r),
-        *_pool_ptrs(c, cache, scales, n_blocks, block_size),
-        _ptr(block_table, "block_table", False, _i32(), B * int(max_blocks)),
-        _ptr(ctx_len, "ctx_len", False, _i32(), B), B, int(max_blocks), int(n_blocks),
-        int(block_size), _ptr(w_o, "w_o", True, dt, H * h * dv),
-        _ptr(out, "out", False, dt, B * (H if w_o is not None else h * dv)),
-        *_ws(workspace, q_nope, q_pe, w_kv_b, cache, scales, block_table, ctx_len, w_o, out),
-        _stream(stream)))
+    qn, qp, w, cc, sc, tb, cx, wo, o, ws, size = _ptrs(workspace, (
+        (q_nope, "q_nope", dt, B * h * dn, False), (q_pe, "q_pe", dt, B * h * dr, False),
+        (w_kv_b, "w_kv_b", dt, h * (dn + dv) * r, False),
+        *_pool(c, cache, scales, n_blocks, block_size),
+        (block_table, "block_table", _I32, B * max_blocks, False),
+        (ctx_len, "ctx_len", _I32, B, False), (w_o, "w_o", dt, H * h * dv, True),
+        (out, "out", dt, B * (H if w_o is not None else h * dv), False)))
+    status = _lib.load().mla_decode_paged(C.byref(c), qn, qp, w, cc, sc, tb, cx, B, max_blocks,
+                                          n_blocks, block_size, wo, o, ws, size,
+                                          _stream_of(stream, workspace))
+    if status:
+        _check(status)

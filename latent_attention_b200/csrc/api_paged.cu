@@ -77,7 +77,7 @@ void paged_layout(const mla_config& c, int B, int max_blocks, int block_size,
     L->split_tokens = mla::pslices::CT;
     L->max_splits = 2 * t.n_units;
     parts = L->max_splits;
-    L->q_lat = take(B * h * r * es);
+    L->q_lat = -1;
     L->q8 = take(rows * 2 * w + rows * 4);     // the terms, then a factor per row
     L->plan = take(((int64_t)B + 1) * 8 + (int64_t)B * 4);
   } else {
@@ -89,7 +89,7 @@ void paged_layout(const mla_config& c, int B, int max_blocks, int block_size,
   }
   L->part_o = take(parts * h * r * 4);
   L->part_lse = take(parts * h * 4);
-  L->o_lat = take(B * h * r * es);
+  L->o_lat = take(B * h * r * (mla::tc_paged_supported(c) ? 4 : es));
   L->o = take(B * h * c.v_head_dim * es);
   L->total_bytes = off;
 }
@@ -244,7 +244,9 @@ mla_status mla_decode_paged(const mla_config* cfg, const void* q_nope, const voi
   if (s != MLA_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;
   char* ws = static_cast<char*>(workspace);
-  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+  const bool tc = mla::tc_paged_supported(c);
+  cudaError_t e = cudaSuccess;
+  if (!tc) e = cudaMemsetAsync(ws, 0, 256, st);     // else the first kernel clears the status
   if (e != cudaSuccess) return cuda_fail(e, "memset");
   mla::stage_event(0, st);
   mla::PagedDecodeArgs a{};
@@ -255,12 +257,12 @@ mla_status mla_decode_paged(const mla_config* cfg, const void* q_nope, const voi
   a.dr = c.qk_rope_head_dim; a.dv = c.v_head_dim; a.r = c.kv_lora_rank;
   a.scale = (float)mla::softmax_scale(c);
   a.split_tokens = L.split_tokens; a.max_splits = L.max_splits;
-  a.q_lat = ws + L.q_lat;
+  a.q_lat = tc ? nullptr : ws + L.q_lat;
   a.part_o = (float*)(ws + L.part_o); a.part_lse = (float*)(ws + L.part_lse);
   a.o_lat = ws + L.o_lat;
   a.o = w_o ? ws + L.o : out;
   a.status = (uint32_t*)(ws + L.status);
-  if (mla::tc_paged_supported(c)) {
+  if (tc) {
     a.tc = mla::tc_paged_plan(a.h, L.max_splits / 2);
     const int64_t rows = (int64_t)B * a.tc.groups * a.tc.NH;
     a.tc.n_units = L.max_splits / 2;

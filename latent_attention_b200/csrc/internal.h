@@ -163,7 +163,7 @@ struct PagedDecodeArgs {
   void* o_lat;                     // [B, h, r]
   void* o;                         // [B, h, dv]
   uint32_t* status;
-  // tensor cores: q_lat is [B, h, r], the partials [2 n_units, h, ...]
+  // tensor cores: no q_lat, o_lat in fp32, the partials [2 n_units, h, ...]
   PagedTcPlan tc;
   uint8_t* q8;                     // [B, groups, 2, NH, r + dr] e4m3 terms
   float* qf;                       // [B, groups, NH]

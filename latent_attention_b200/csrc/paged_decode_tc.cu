@@ -1,14 +1,13 @@
 // Weight-absorbed decode over the paged 8-bit latent cache on sm_100a tensor
 // cores (bf16 model, latent 512 + rope 64).
 //
-//   P1 q_lat[b,h] = W_UK[h]^T q_nope[b,h]          batched tcgen05 GEMM
-//   P2 paged_query_kernel   [q_lat | q_pe] as two e4m3 terms and a power of
-//                           two per head; the chunk line of all sequences
-//   P3 paged_attn_kernel    attention over the blocks (below)
-//   P4 paged_combine_kernel merge of the partial results of cut sequences
-//   P5 o[b,h] = W_UV[h] o_lat[b,h]                 batched tcgen05 GEMM
+//   P1 paged_query_kernel   q_lat = W_UK^T q_nope; [q_lat | q_pe] as two e4m3
+//                           terms and a power of two per head (paged_proj.cu)
+//   P2 paged_attn_kernel    attention over the blocks (below)
+//   P3 paged_output_kernel  merge of the partial results of cut sequences,
+//                           o = W_UV o_lat (paged_proj.cu)
 //
-// P3.  The blocks' bytes are MMA operands as they lie in memory: no value is
+// P2.  The blocks' bytes are MMA operands as they lie in memory: no value is
 // converted on the way.  What multiplies them is e4m3 too, as a sum hi + lo of
 // two e4m3 terms (together 8 significant bits, bf16's precision), so a product
 // takes two 8-bit MMAs, the time of one bf16 MMA, and half the bytes.
@@ -25,12 +24,12 @@
 //
 // Softmax.  A thread is a token; it holds the scores of 16 heads.
 // s = raw 2^e_block f_head (log2 units); p = 2^(s - ref_head); its share of a
-// row sum stays in the thread until the segment ends.  ref is the maximum of the
-// segment's first chunk and moves only when a score passes it by 2^kGrow, so
-// no chunk waits for O to be rescaled.  What the MMA takes is p 2^e_block
-// (the bytes' own scale), which spans more than e4m3 does (a few tokens may
-// hold half of the weight and thousands the rest), so every 32 tokens of a
-// head carry a power of two of their own: kind::mxf8f6f4 multiplies it in
+// row sum stays in the thread until the segment ends.  ref is the score of
+// the segment's first token and moves only when a score passes it by kGrow
+// (to the chunk's maximum), so hardly a chunk waits for O to be rescaled.  What
+// the MMA takes is p 2^e_block (the bytes' own scale), which spans more than
+// e4m3 does (a few tokens may hold half of the weight and thousands the rest),
+// so every 32 tokens of a head carry a power of two of their own: kind::mxf8f6f4 multiplies it in
 // (a ue8m0 scale per head and 32 values of K), and hi + lo keep 8 bits of
 // everything within 2^-10 of the largest of the 32, nothing below 2^-18 of it.
 //
@@ -125,7 +124,7 @@ struct AttnParams {
   int n_units, min_len;
   float* part_o;               // [2 n_units, h, R]
   float* part_lse;             // [2 n_units, h], log2
-  __nv_bfloat16* o_lat;        // [B, h, R]
+  float* o_lat;                // [B, h, R], sequences in one segment
   uint32_t* status;
 };
 
@@ -264,115 +263,7 @@ __device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
-// --------------------------------------------------- P2: query and schedule
-// Row (b, group, i < NH) of q8: hi at ((b G + g) 2) NH + i, lo NH rows later;
-// 576 bytes each.  value = (hi + lo) 2^e with max |value| in (224, 448] 2^e.
-struct QueryParams {
-  const __nv_bfloat16 *q_lat, *q_pe;       // [B, h, R], [B, h, DR]
-  uint8_t* q8;
-  float* qf;
-  const int32_t* ctx;
-  int64_t* pre;
-  int32_t* len;
-  int B, h, groups, hg_heads, NH;
-  int64_t most;                            // tokens a table holds
-  float scale_log2;
-  uint32_t* status;
-};
-constexpr int kQueryThreads = 256;
-
-__device__ __forceinline__ void split8(const float (&v)[16], float f, uint4& hi, uint4& lo) {
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float x[4], y[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = v[4 * i + k] * f;
-    h[i] = to_e4m3x4(x[0], x[1], x[2], x[3]);
-    from_e4m3x4(h[i], y);
-    l[i] = to_e4m3x4(x[0] - y[0], x[1] - y[1], x[2] - y[2], x[3] - y[3]);
-  }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
-__global__ void __launch_bounds__(kQueryThreads) paged_query_kernel(QueryParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (blockIdx.x == 0) {                   // lengths and the chunk line
-    __shared__ int64_t sums[kQueryThreads / 32];
-    const int per = (p.B + kQueryThreads - 1) / kQueryThreads;
-    const int b0 = min(t * per, p.B), b1 = min(b0 + per, p.B);
-    int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      int64_t n = p.ctx[b];
-      if (n < 0 || n > p.most) {
-        atomicOr(p.status, kStatusBadPage);
-        n = n < 0 ? 0 : p.most;
-      }
-      p.len[b] = (int32_t)n;
-      sum += charged(n);
-    }
-    int64_t inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
-    }
-    if (lane == 31) sums[warp] = inc;
-    __syncthreads();
-    int64_t at = inc - sum;
-    for (int w = 0; w < warp; ++w) at += sums[w];
-    for (int b = b0; b < b1; ++b) {
-      at += charged(p.len[b]);
-      p.pre[b + 1] = at;
-    }
-    if (t == 0) p.pre[0] = 0;
-    return;
-  }
-  const int64_t row = (int64_t)(blockIdx.x - 1) * (kQueryThreads / 32) + warp;
-  if (row >= (int64_t)p.B * p.groups * p.NH) return;
-  const int i = (int)(row % p.NH);
-  const int64_t bg = row / p.NH;
-  const int g = (int)(bg % p.groups), head = g * p.hg_heads + i;
-  const int64_t b = bg / p.groups;
-  uint8_t* hi_row = p.q8 + (bg * 2 * p.NH + i) * W;
-  uint8_t* lo_row = hi_row + (int64_t)p.NH * W;
-  float v[16], r[2] = {0.f, 0.f};
-#pragma unroll
-  for (int k = 0; k < 16; ++k) v[k] = 0.f;
-  if (i < p.hg_heads && head < p.h) {
-    load16(p.q_lat + (b * p.h + head) * R + lane * 16, v);
-    const uint32_t x =
-        reinterpret_cast<const uint32_t*>(p.q_pe + (b * p.h + head) * DR)[lane];
-    r[0] = __uint_as_float(x << 16);
-    r[1] = __uint_as_float(x & 0xffff0000u);
-  }
-  uint32_t amax = 0;
-#pragma unroll
-  for (int k = 0; k < 18; ++k) {
-    float& x = k < 16 ? v[k] : r[k - 16];
-    const uint32_t a = __float_as_uint(x) & 0x7fffffffu;
-    // an infinity becomes NaN (e4m3 has none), and does not set the scale
-    if (a < 0x7f800000u) amax = max(amax, a); else x = x - x;
-  }
-  const int e = scale_exp(__reduce_max_sync(0xffffffffu, amax));
-  const float f = pow2(-e);
-  uint4 hi, lo;
-  split8(v, f, hi, lo);
-  reinterpret_cast<uint4*>(hi_row)[lane] = hi;
-  reinterpret_cast<uint4*>(lo_row)[lane] = lo;
-  const uint32_t rh = to_e4m3x2(r[0] * f, r[1] * f);
-  float y[4];
-  from_e4m3x4(rh, y);
-  reinterpret_cast<uint16_t*>(hi_row + R)[lane] = (uint16_t)rh;
-  reinterpret_cast<uint16_t*>(lo_row + R)[lane] =
-      (uint16_t)to_e4m3x2(r[0] * f - y[0], r[1] * f - y[1]);
-  if (lane == 0) p.qf[row] = p.scale_log2 * pow2(e);
-}
-
-// ------------------------------------------------------------- P3: attention
+// ------------------------------------------------------------- P2: attention
 // First sequence whose charged chunks reach past r, by a whole warp: every
 // round narrows the range 32-fold.
 __device__ __forceinline__ int seq_at_warp(const int64_t* pre, int B, int64_t r, int lane) {
@@ -739,9 +630,24 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
 #pragma unroll
           for (int i = 0; i < HPG; ++i) v[i] = -INFINITY;
         }
-        // the rare case: the segment's first chunk, or a score far above its
-        // reference (or a warp that gave up)
-        const bool far = barrier_or(bar, 128, j == 0 || !ok || (live && vm > kGrow));
+        if (j == 0) {
+          // the first token's scores are the segment's first references (nref
+          // may still be read as 0 by a slower warp before the barrier)
+          if (row == 0) {
+#pragma unroll
+            for (int i = 0; i < HPG; ++i) sh.alpha[h0 + i] = -v[i];
+          }
+          named_barrier_sync(bar, 128);
+          if (tg < HPG) sh.nref[h0 + tg] = sh.alpha[h0 + tg];
+          vm = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < HPG; ++i) {
+            v[i] += sh.alpha[h0 + i];
+            vm = fmaxf(vm, v[i]);
+          }
+        }
+        // the rare case: a score far above its reference (or a warp that gave up)
+        const bool far = barrier_or(bar, 128, !ok || (live && vm > kGrow));
         uint32_t m[HPG / 2];
         int pair;                             // of heads whose maximum this lane ends with
         bool leave = false;
@@ -790,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
           if (quad == 0 && lane < HPG) {
             const float x = key_float(max(max(sh.hmax[grp][0][lane], sh.hmax[grp][1][lane]),
                                           max(sh.hmax[grp][2][lane], sh.hmax[grp][3][lane])));
-            const float old = j == 0 ? x : -sh.nref[h0 + lane], now = x > old ? x : old;
+            const float old = -sh.nref[h0 + lane], now = x > old ? x : old;
             sh.nref[h0 + lane] = -now;
             sh.alpha[h0 + lane] = ex2(old - now);
           }
@@ -916,15 +822,14 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
             if (lane == 0) mbar_arrive(&sh.o_free);
           }
           const int dim = a * 128 + row;
-          __nv_bfloat16* dl = p.o_lat + ((int64_t)s.b * p.h + head0) * R + dim;
-          float* dp = p.part_o + ((int64_t)s.slot * p.h + head0) * R + dim;
+          float* dst = (s.whole ? p.o_lat + ((int64_t)s.b * p.h + head0) * R
+                                : p.part_o + ((int64_t)s.slot * p.h + head0) * R) + dim;
 #pragma unroll
           for (int k = 0; k < HPG; ++k) {
             if (k >= n_heads) continue;
             float x = __uint_as_float(o[k]);
             if (K::STK) x += __uint_as_float(o2[k]);
-            x *= sh.alpha[h0 + k];
-            if (s.whole) dl[k * R] = __float2bfloat16(x); else dp[k * R] = x;
+            dst[k * R] = x * sh.alpha[h0 + k];
           }
         }
       }
@@ -937,44 +842,6 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
     tc_fence_after();
     tmem_dealloc(tbase, K::TM_COLS);
   }
-}
-
-// P4: o_lat[b, h] of a sequence that several units hold, from their partials
-// (weights 2^(lse - max)); zeros for one without tokens.  A warp per (b, h),
-// 16 dims a lane.
-constexpr int kCombineWarps = 4;
-__global__ void __launch_bounds__(32 * kCombineWarps)
-    paged_combine_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse,
-                         __nv_bfloat16* __restrict__ o_lat, const int64_t* __restrict__ pre, int B,
-                         int h, int n_units, int min_len) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t row = (int64_t)blockIdx.x * kCombineWarps + threadIdx.x / 32;
-  if (row >= (int64_t)B * h) return;
-  const int b = (int)(row / h), hh = (int)(row % h), at = (threadIdx.x % 32) * 16;
-  float acc[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  if (pre[b + 1] != pre[b]) {
-    const SeqUnits su = seq_units(pre, b, B, n_units, min_len);
-    if (su.u0 == su.u1) return;            // the attention kernel wrote it
-    float mx = -INFINITY;
-    for (int uu = su.u0; uu <= su.u1; ++uu)
-      mx = fmaxf(mx, part_lse[(int64_t)seq_slot(su, uu) * h + hh]);
-    float den = 0.f;
-    for (int uu = su.u0; uu <= su.u1; ++uu) {
-      const int64_t part = (int64_t)seq_slot(su, uu) * h + hh;
-      const float w = exp2f(part_lse[part] - mx);
-      float v[16];
-      load16(part_o + part * R + at, v);
-      den += w;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, v[i], acc[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] /= den;
-  }
-  store16(o_lat + row * R + at, acc);
 }
 
 template <int NH>
@@ -996,91 +863,48 @@ PagedTcPlan tc_paged_plan(int h, int sms) {
   t.groups = (h + 63) / 64;
   t.hg_heads = (h + t.groups - 1) / t.groups;
   t.NH = (t.hg_heads + 15) / 16 * 16;
-  t.n_units = sms / t.groups > 0 ? sms / t.groups : 1;
+  const int n = sms / t.groups;
+  t.n_units = n < 1 ? 1 : n > 512 ? 512 : n;   // 512: what the output kernel merges
   return t;
 }
 
 cudaError_t tc_paged_decode(const PagedDecodeArgs& a, cudaStream_t st) {
-  cudaError_t e;
   const PagedTcPlan& t = a.tc;
-  {
-    GemmArgs g;
-    g.A = a.q_nope; g.lda = (int64_t)a.h * a.dn; g.sA = a.dn; g.a_batch_inner = true;
-    g.Bm[0] = a.w_kv_b; g.ldb[0] = R; g.sB = (int64_t)(a.dn + a.dv) * R; g.b_mn = true;
-    g.M = a.B; g.K = a.dn; g.batch = a.h; g.nseg = 1;
-    g.seg[0].out = a.q_lat; g.seg[0].ldo = (int64_t)a.h * R; g.seg[0].ncols = R;
-    g.sOut = R;
-    if (!tc_gemm_supported(g, MLA_BF16)) return cudaErrorNotSupported;
-    e = tc_gemm(g, st, a.status);
-    if (e != cudaSuccess) return e;
-  }
-  const int64_t rows = (int64_t)a.B * t.groups * t.NH;
-  {
-    QueryParams q;
-    q.q_lat = (const __nv_bfloat16*)a.q_lat;
-    q.q_pe = (const __nv_bfloat16*)a.q_pe;
-    q.q8 = a.q8; q.qf = a.qf; q.ctx = a.ctx; q.pre = a.pre; q.len = a.len;
-    q.B = a.B; q.h = a.h; q.groups = t.groups; q.hg_heads = t.hg_heads; q.NH = t.NH;
-    q.most = (int64_t)a.max_blocks * a.pool.bs;
-    q.scale_log2 = a.scale * 1.4426950408889634f;
-    q.status = a.status;
-    const int64_t per = kQueryThreads / 32;
-    e = launch_pdl(paged_query_kernel, dim3((unsigned)(1 + (rows + per - 1) / per)),
-                   dim3(kQueryThreads), 0, st, q);
-    count_launches();
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e = launch_paged_query(a, st);
+  if (e != cudaSuccess) return e;
   stage_event(1, st);
+  // e4m3 tensors as pairs of bytes: 288 columns of 16 bits
+  CUtensorMap tmQ, tmQr, tmC, tmCr;
+  const uint64_t str[1] = {(uint64_t)W};
+  const uint64_t qdims[2] = {W / 2, (uint64_t)a.B * t.groups * 2 * t.NH};
+  const uint32_t qbox[2] = {64, (uint32_t)(2 * t.NH)}, qrbox[2] = {DR / 2, (uint32_t)(2 * t.NH)};
+  const uint64_t cdims[2] = {W / 2, (uint64_t)a.pool.n_blocks * a.pool.bs};
+  const uint32_t cbox[2] = {64, (uint32_t)a.pool.bs}, crbox[2] = {DR / 2, (uint32_t)a.pool.bs};
+  if (!encode_tmap(&tmQ, a.q8, 2, qdims, str, qbox) ||
+      !encode_tmap(&tmQr, a.q8, 2, qdims, str, qrbox, 64) ||
+      !encode_tmap(&tmC, a.pool.cache, 2, cdims, str, cbox) ||
+      !encode_tmap(&tmCr, a.pool.cache, 2, cdims, str, crbox, 64))
+    return cudaErrorInvalidValue;
   AttnParams p{};
-  {
-    // e4m3 tensors as pairs of bytes: 288 columns of 16 bits
-    CUtensorMap tmQ, tmQr, tmC, tmCr;
-    const uint64_t str[1] = {(uint64_t)W};
-    const uint64_t qdims[2] = {W / 2, (uint64_t)rows * 2};
-    const uint32_t qbox[2] = {64, (uint32_t)(2 * t.NH)}, qrbox[2] = {DR / 2, (uint32_t)(2 * t.NH)};
-    const uint64_t cdims[2] = {W / 2, (uint64_t)a.pool.n_blocks * a.pool.bs};
-    const uint32_t cbox[2] = {64, (uint32_t)a.pool.bs}, crbox[2] = {DR / 2, (uint32_t)a.pool.bs};
-    if (!encode_tmap(&tmQ, a.q8, 2, qdims, str, qbox) ||
-        !encode_tmap(&tmQr, a.q8, 2, qdims, str, qrbox, 64) ||
-        !encode_tmap(&tmC, a.pool.cache, 2, cdims, str, cbox) ||
-        !encode_tmap(&tmCr, a.pool.cache, 2, cdims, str, crbox, 64))
-      return cudaErrorInvalidValue;
-    p.pre = a.pre; p.len = a.len; p.table = a.table;
-    p.cache = a.pool.cache; p.scales = a.pool.scales; p.qf = a.qf;
-    p.B = a.B; p.max_blocks = a.max_blocks; p.n_blocks = a.pool.n_blocks; p.bs = a.pool.bs;
-    p.lbs = a.pool.bs == 16 ? 4 : a.pool.bs == 32 ? 5 : a.pool.bs == 64 ? 6 : 7;
-    p.h = a.h; p.groups = t.groups; p.hg_heads = t.hg_heads;
-    p.n_units = t.n_units; p.min_len = 1;
-    p.part_o = a.part_o; p.part_lse = a.part_lse;
-    p.o_lat = (__nv_bfloat16*)a.o_lat;
-    p.status = a.status;
-    e = t.NH == 16   ? launch_attn<16>(p, tmQ, tmQr, tmC, tmCr, st)
-        : t.NH == 32 ? launch_attn<32>(p, tmQ, tmQr, tmC, tmCr, st)
-        : t.NH == 48 ? launch_attn<48>(p, tmQ, tmQr, tmC, tmCr, st)
-                     : launch_attn<64>(p, tmQ, tmQr, tmC, tmCr, st);
-    count_launches();
-    if (e != cudaSuccess) return e;
-  }
-  stage_event(2, st);
-  e = launch_pdl(paged_combine_kernel,
-                 dim3((unsigned)(((int64_t)a.B * a.h + kCombineWarps - 1) / kCombineWarps)),
-                 dim3(32 * kCombineWarps), 0, st, (const float*)a.part_o, (const float*)a.part_lse,
-                 (__nv_bfloat16*)a.o_lat, (const int64_t*)a.pre, a.B, a.h, p.n_units, p.min_len);
+  p.pre = a.pre; p.len = a.len; p.table = a.table;
+  p.cache = a.pool.cache; p.scales = a.pool.scales; p.qf = a.qf;
+  p.B = a.B; p.max_blocks = a.max_blocks; p.n_blocks = a.pool.n_blocks; p.bs = a.pool.bs;
+  p.lbs = a.pool.bs == 16 ? 4 : a.pool.bs == 32 ? 5 : a.pool.bs == 64 ? 6 : 7;
+  p.h = a.h; p.groups = t.groups; p.hg_heads = t.hg_heads;
+  p.n_units = t.n_units; p.min_len = 1;
+  p.part_o = a.part_o; p.part_lse = a.part_lse;
+  p.o_lat = (float*)a.o_lat;
+  p.status = a.status;
+  e = t.NH == 16   ? launch_attn<16>(p, tmQ, tmQr, tmC, tmCr, st)
+      : t.NH == 32 ? launch_attn<32>(p, tmQ, tmQr, tmC, tmCr, st)
+      : t.NH == 48 ? launch_attn<48>(p, tmQ, tmQr, tmC, tmCr, st)
+                   : launch_attn<64>(p, tmQ, tmQr, tmC, tmCr, st);
   count_launches();
   if (e != cudaSuccess) return e;
+  stage_event(2, st);
+  e = launch_paged_output(a, p.min_len, st);
+  if (e != cudaSuccess) return e;
   stage_event(3, st);
-  {
-    GemmArgs g;
-    g.A = a.o_lat; g.lda = (int64_t)a.h * R; g.sA = R; g.a_batch_inner = true;
-    g.Bm[0] = reinterpret_cast<const __nv_bfloat16*>(a.w_kv_b) + (int64_t)a.dn * R;
-    g.ldb[0] = R; g.sB = (int64_t)(a.dn + a.dv) * R;
-    g.M = a.B; g.K = R; g.batch = a.h; g.nseg = 1;
-    g.seg[0].out = a.o; g.seg[0].ldo = (int64_t)a.h * a.dv; g.seg[0].ncols = a.dv;
-    g.sOut = a.dv;
-    if (!tc_gemm_supported(g, MLA_BF16)) return cudaErrorNotSupported;
-    e = tc_gemm(g, st, a.status);
-    if (e != cudaSuccess) return e;
-  }
   return cudaGetLastError();
 }
 

@@ -446,7 +446,13 @@ def test_decode_no_tokens_at_all(cuda):
 @pytest.mark.parametrize("heads", [4, 40, 128])
 def test_decode_one_dominant_token_over_a_flat_background(cuda, heads):
     """Scores that put half of the weight on one token and spread the other
-    half over thousands that all point the same way: small weights count."""
+    half over thousands that all point the same way: small weights count.
+
+    The two halves nearly cancel (0.39 of a row of -1 against 0.61 of rows
+    around 0.6), so the error is held against what is summed, not only
+    against what is left: a weight rounded to 8 significant bits is off by up
+    to 2^-8 of itself, and all equal weights alike, which moves the output by
+    up to 2^-8 sum_j p_j |W_UV c_j|."""
     cfg, bs, n = bf16(heads), 64, 9000
     d = decode_inputs(cfg, [n], bs, 3, spread=0.0)
     d["q_nope"].zero_()
@@ -463,7 +469,14 @@ def test_decode_one_dominant_token_over_a_flat_background(cuda, heads):
     d["cache"] = (x / 0.125).to(FP8).view(torch.uint8)
     d["scales"] = torch.full((d["n_blocks"],), 0.125)
     out, _ = run_decode_paged(cfg, d, bs)
-    assert oracle.max_rel_err(out, want_decode(cfg, d, bs)) <= TOL["bf16"]
+    want = want_decode(cfg, d, bs)
+    rows = O.rows_of(d["cache"].numpy(), d["scales"].numpy(), d["table"], d["ctx"], 0, bs)
+    e = np.exp(8.0 * scale * (rows[:, 512] - rows[:, 512].max()))
+    w_uv = f64(d["w"]).reshape(heads, 256, 512)[:, 128:]
+    summed = max((np.abs(rows[:, :512] @ w_uv[h].T) * (e / e.sum())[:, None]).sum(0).max()
+                 for h in range(heads))
+    err = np.abs(f64(out) - want).max()
+    assert err <= TOL["bf16"] * np.abs(want).max() + 2.0 ** -8 * summed
 
 
 @pytest.mark.parametrize("cfg", [F32, bf16(24), bf16(128)], ids=["f32", "h24", "h128"])
