@@ -60,7 +60,14 @@ mla::PagedPool pool_of(const mla_config& c, const void* cache, const float* scal
   return p;
 }
 
-constexpr int kSimtSplit = 1024;      // tokens per split on CUDA cores
+// Tokens per split on CUDA cores: enough splits for some sixteen blocks an SM,
+// between 64 tokens (a block's threads) and 1024 (its partial result, r floats,
+// stays small beside the r-byte rows that it sums).
+constexpr int kSimtSplit = 1024;
+int simt_split(const mla_config& c, int64_t B, int64_t max_ctx) {
+  const int64_t want = B * c.num_heads * max_ctx / (16ll * mla::device_sms());
+  return (int)std::min<int64_t>(kSimtSplit, std::max<int64_t>(64, (want + 63) / 64 * 64));
+}
 
 void paged_layout(const mla_config& c, int B, int max_blocks, int block_size,
                   mla_paged_layout* L) {
@@ -81,8 +88,8 @@ void paged_layout(const mla_config& c, int B, int max_blocks, int block_size,
     L->q8 = take(rows * 2 * w + rows * 4);     // the terms, then a factor per row
     L->plan = take(((int64_t)B + 1) * 8 + (int64_t)B * 4);
   } else {
-    L->split_tokens = kSimtSplit;
-    L->max_splits = (int32_t)((max_ctx + kSimtSplit - 1) / kSimtSplit);
+    L->split_tokens = simt_split(c, B, max_ctx);
+    L->max_splits = (int32_t)((max_ctx + L->split_tokens - 1) / L->split_tokens);
     parts = (int64_t)B * L->max_splits;
     L->q_lat = take(B * h * w * es);
     L->q8 = L->plan = -1;
@@ -100,7 +107,7 @@ mla_status check_decode(const mla_config& c, bool o_proj, int max_blocks, int bl
   if (s != MLA_OK) return s;
   const int w = c.kv_lora_rank + c.qk_rope_head_dim;
   if (mla::tc_paged_supported(c)) return MLA_OK;
-  if (std::max(mla::paged_simt_smem(w, kSimtSplit), 4 * c.kv_lora_rank) > mla::kMaxSmem)
+  if (std::max(mla::paged_simt_smem(w, kSimtSplit), 4 * (c.kv_lora_rank + 256)) > mla::kMaxSmem)
     return fail(MLA_ERR_UNSUPPORTED, "paged decode: kv_lora_rank + qk_rope_head_dim = %d is too large", w);
   if ((int64_t)max_blocks * block_size > 65535ll * kSimtSplit)
     return fail(MLA_ERR_UNSUPPORTED, "paged decode: max_blocks x block_size > %lld tokens",
@@ -245,10 +252,8 @@ mla_status mla_decode_paged(const mla_config* cfg, const void* q_nope, const voi
   cudaStream_t st = (cudaStream_t)stream;
   char* ws = static_cast<char*>(workspace);
   const bool tc = mla::tc_paged_supported(c);
-  cudaError_t e = cudaSuccess;
-  if (!tc) e = cudaMemsetAsync(ws, 0, 256, st);     // else the first kernel clears the status
-  if (e != cudaSuccess) return cuda_fail(e, "memset");
-  mla::stage_event(0, st);
+  cudaError_t e;
+  mla::stage_event(0, st);                // the first kernel clears the status word
   mla::PagedDecodeArgs a{};
   a.q_nope = q_nope; a.q_pe = q_pe; a.w_kv_b = w_kv_b;
   a.pool = pool_of(c, cache, scales, n_blocks, block_size);

@@ -251,11 +251,11 @@ cudaError_t launch_paged_append(int dtype, const void* rows, const int32_t* slot
 cudaError_t launch_paged_gather(int dtype, const PagedPool& pool, const int32_t* table,
                                 const int32_t* ctx, void* rows, int32_t* cu, int B,
                                 int max_blocks, int capacity, uint32_t* status, cudaStream_t st);
-// Shared memory of the CUDA-core paged decode: the query, the split's scores
-// and, per 16 tokens, a scale and a block id.
+// Shared memory of the CUDA-core paged decode: the query, 1024 partial sums,
+// the split's scores and, per 16 tokens, a scale and a block id.
 constexpr int kMaxSmem = 227 * 1024 - 1024;
 inline int paged_simt_smem(int w, int split_tokens) {
-  return 4 * (w + split_tokens + 2 * (split_tokens / 16));
+  return 4 * (w + 1024 + split_tokens + 2 * (split_tokens / 16));
 }
 cudaError_t launch_paged_decode_simt(int dtype, const PagedDecodeArgs& a, cudaStream_t st);
 // Smallest workspace mla_decode_absorbed runs with (one SM pair on tensor cores).

@@ -5,6 +5,7 @@
 //   statistics and sums over splits of the context           (split kernel)
 //   log-sum-exp merge of the splits, o = W_UV[h] o_lat       (merge kernel)
 #include "paged.cuh"
+#include "sm100.cuh"
 
 namespace mla {
 namespace {
@@ -13,6 +14,9 @@ using namespace paged;
 
 template <typename T>
 __global__ void paged_absorb_kernel(PagedDecodeArgs a) {
+  sm100::griddep_wait();
+  sm100::griddep_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
   const int b = blockIdx.x, hh = blockIdx.y;
   extern __shared__ float qn[];
   const T* qnope = reinterpret_cast<const T*>(a.q_nope) + ((int64_t)b * a.h + hh) * a.dn;
@@ -38,28 +42,32 @@ __device__ __forceinline__ int tokens_of(const PagedDecodeArgs& a, int b) {
   return n < 0 ? 0 : (int)most;
 }
 
-// One block per (sequence, head, split): the split's rows are found once, a
-// warp scores a token, then every thread owns latent columns.
+// One block per (sequence, head, split of the context): four threads share a
+// token's dot product (16-byte pieces in turn), then a thread owns four latent
+// columns of every tl-th token.
+constexpr int kThreads = 256;
+
 template <typename T>
-__global__ void paged_split_kernel(PagedDecodeArgs a) {
-  const int b = blockIdx.x, hh = blockIdx.y, sp = blockIdx.z;
+__global__ void __launch_bounds__(kThreads) paged_split_kernel(PagedDecodeArgs a) {
+  sm100::griddep_wait();
+  sm100::griddep_launch_dependents();
+  const int b = blockIdx.x, hh = blockIdx.y, sp = blockIdx.z, tid = threadIdx.x;
   const int n = tokens_of(a, b), t0 = sp * a.split_tokens;
   const int64_t part = ((int64_t)b * a.max_splits + sp) * a.h + hh;
-  if (t0 >= n) {                              // empty split: neutral partial
-    for (int c = threadIdx.x; c < a.r; c += blockDim.x) a.part_o[part * a.r + c] = 0.f;
-    if (threadIdx.x == 0) a.part_lse[part] = -INFINITY;
+  if (t0 >= n) {                              // empty split: the merge skips it
+    if (tid == 0) a.part_lse[part] = -INFINITY;
     return;
   }
   const int nt = min(n - t0, a.split_tokens), w = a.pool.W, bs = a.pool.bs;
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   float* q = sm;                              // [w]
-  float* s = q + w;                           // [split_tokens] scores, then weights
+  float* red = q + w;                         // [4 kThreads] sums of the token lanes
+  float* s = red + 4 * kThreads;              // [split_tokens] scores, then weights
   float* scl = s + a.split_tokens;            // [split_tokens / 16] scale of every 16 tokens
   int* blk = reinterpret_cast<int*>(scl + a.split_tokens / 16);   // their block
-  __shared__ float red[32];
+  __shared__ float part_max[32], part_sum[32];
   const T* ql = reinterpret_cast<const T*>(a.q_lat) + ((int64_t)b * a.h + hh) * w;
-  for (int c = threadIdx.x; c < w; c += blockDim.x) q[c] = Elem<T>::load(ql + c);
-  for (int g = threadIdx.x; g < (nt + 15) / 16; g += blockDim.x) {
+  for (int g = tid; g < (nt + 15) / 16; g += kThreads) {
     int id = a.table[(int64_t)b * a.max_blocks + (t0 + 16 * g) / bs];
     if (id < 0 || id >= a.pool.n_blocks) {
       atomicOr(a.status, kStatusBadPage);
@@ -68,79 +76,134 @@ __global__ void paged_split_kernel(PagedDecodeArgs a) {
     blk[g] = id;
     scl[g] = a.pool.scales[id];
   }
+  for (int c = tid; c < w; c += kThreads) q[c] = Elem<T>::load(ql + c);
   __syncthreads();
   auto row = [&](int t) {
     return a.pool.cache + ((int64_t)blk[t >> 4] * bs + (t0 + t) % bs) * w;
   };
-  auto value = [](const uint8_t* p) {
-    float f[4];
-    from_e4m3x4(*p, f);
-    return f[0];
-  };
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, nw = blockDim.x / 32;
-  for (int t = warp; t < nt; t += nw) {
-    const uint8_t* c8 = row(t);
-    float acc = 0.f;
-    for (int c = lane; c < w; c += 32) acc = fmaf(q[c], value(c8 + c), acc);
-    for (int o = 16; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) s[t] = acc * scl[t >> 4] * a.scale;
-  }
-  __syncthreads();
+  const int warp = tid / 32, lane = tid % 32;
   float mx = -INFINITY;
-  for (int t = threadIdx.x; t < nt; t += blockDim.x) mx = fmaxf(mx, s[t]);
+  for (int tb = 0; tb < nt; tb += kThreads / 4) {
+    const int t = tb + tid / 4;
+    float acc = 0.f;
+    if (t < nt) {
+      const uint8_t* c8 = row(t);
+      for (int c = (tid & 3) * 16; c < w; c += 64) {
+        float v[16];
+        dequant16(*reinterpret_cast<const uint4*>(c8 + c), 1.f, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(q + c + 4 * i);
+          acc = fmaf(x.x, v[4 * i], acc);
+          acc = fmaf(x.y, v[4 * i + 1], acc);
+          acc = fmaf(x.z, v[4 * i + 2], acc);
+          acc = fmaf(x.w, v[4 * i + 3], acc);
+        }
+      }
+    }
+    acc += __shfl_xor_sync(0xffffffffu, acc, 1);
+    acc += __shfl_xor_sync(0xffffffffu, acc, 2);
+    if (t < nt) {
+      acc *= scl[t >> 4] * a.scale;
+      if ((tid & 3) == 0) s[t] = acc;
+      mx = fmaxf(mx, acc);
+    }
+  }
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) red[warp] = mx;
+  if (lane == 0) part_max[warp] = mx;
   __syncthreads();
   mx = -INFINITY;
-  for (int i = 0; i < nw; ++i) mx = fmaxf(mx, red[i]);
-  __syncthreads();
+  for (int i = 0; i < kThreads / 32; ++i) mx = fmaxf(mx, part_max[i]);
   float l = 0.f;
-  for (int t = threadIdx.x; t < nt; t += blockDim.x) {
+  for (int t = tid; t < nt; t += kThreads) {
     const float p = expf(s[t] - mx);
     s[t] = p * scl[t >> 4];                   // the weight of the row's e4m3 values
     l += p;
   }
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (lane == 0) red[warp] = l;
+  if (lane == 0) part_sum[warp] = l;
   __syncthreads();
   l = 0.f;
-  for (int i = 0; i < nw; ++i) l += red[i];
-  for (int c = threadIdx.x; c < a.r; c += blockDim.x) {
-    float o = 0.f;
-    for (int t = 0; t < nt; ++t) o = fmaf(s[t], value(row(t) + c), o);
-    a.part_o[part * a.r + c] = o / l;
+  for (int i = 0; i < kThreads / 32; ++i) l += part_sum[i];
+  if (tid == 0) a.part_lse[part] = mx + logf(l);
+  const float inv = 1.f / l;
+  // column groups of four in rounds of up to kThreads; r % 4 columns at the
+  // end read past them into the rope part, which is not stored
+  const int groups = (a.r + 3) / 4;
+  for (int g0 = 0; g0 < groups; g0 += kThreads) {
+    const int ng = min(groups - g0, kThreads), tl = kThreads / ng;
+    const int cg = tid % ng, ti = tid / ng;
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    if (ti < tl) {
+      for (int t = ti; t < nt; t += tl) {
+        float v[4];
+        from_e4m3x4(*reinterpret_cast<const uint32_t*>(row(t) + 4 * (g0 + cg)), v);
+        const float p = s[t];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = fmaf(p, v[k], o[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) red[(ti * ng + cg) * 4 + k] = o[k];
+    }
+    __syncthreads();
+    for (int c = tid; c < 4 * ng; c += kThreads) {
+      float x = 0.f;
+      for (int i = 0; i < tl; ++i) x += red[i * ng * 4 + c];
+      if (4 * g0 + c < a.r) a.part_o[part * a.r + 4 * g0 + c] = x * inv;
+    }
+    __syncthreads();
   }
-  if (threadIdx.x == 0) a.part_lse[part] = mx + logf(l);
 }
 
 // o_lat[b,h] from the splits (zero for a sequence without tokens), then
 // o[b,h] = W_UV[h] o_lat; one block per (sequence, head).
 template <typename T>
-__global__ void paged_merge_kernel(PagedDecodeArgs a) {
-  const int b = blockIdx.x, hh = blockIdx.y;
-  extern __shared__ float ol[];               // [r]
+__global__ void __launch_bounds__(kThreads) paged_merge_kernel(PagedDecodeArgs a) {
+  sm100::griddep_wait();
+  sm100::griddep_launch_dependents();
+  const int b = blockIdx.x, hh = blockIdx.y, tid = threadIdx.x;
+  extern __shared__ __align__(16) float ol[];   // [r], then [kThreads] sums
+  float* red = ol + a.r;
+  __shared__ float part_max[32], part_den[32];
+  const int warp = tid / 32, lane = tid % 32;
+  const int n = tokens_of(a, b), ns = (n + a.split_tokens - 1) / a.split_tokens;
   const int64_t p0 = (int64_t)b * a.max_splits * a.h + hh;
   float mx = -INFINITY;
-  for (int sp = 0; sp < a.max_splits; ++sp) mx = fmaxf(mx, a.part_lse[p0 + (int64_t)sp * a.h]);
-  float den = 0.f;                            // stays 0 without tokens; NaN passes through
-  for (int sp = 0; sp < a.max_splits; ++sp) {
-    const float l = a.part_lse[p0 + (int64_t)sp * a.h];
-    den += l == -INFINITY ? 0.f : expf(l - mx);
-  }
-  for (int c = threadIdx.x; c < a.r; c += blockDim.x) {
-    float o = 0.f;
-    for (int sp = 0; sp < a.max_splits; ++sp) {
-      const int64_t part = p0 + (int64_t)sp * a.h;
-      const float l = a.part_lse[part];
-      if (l != -INFINITY) o = fmaf(expf(l - mx), a.part_o[part * a.r + c], o);
-    }
-    ol[c] = den == 0.f ? 0.f : o / den;
-  }
+  for (int sp = tid; sp < ns; sp += kThreads)
+    mx = fmaxf(mx, a.part_lse[p0 + (int64_t)sp * a.h]);
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) part_max[warp] = mx;
   __syncthreads();
+  mx = -INFINITY;
+  for (int i = 0; i < kThreads / 32; ++i) mx = fmaxf(mx, part_max[i]);
+  float den = 0.f;                            // stays 0 without tokens; NaN passes through
+  for (int sp = tid; sp < ns; sp += kThreads) den += expf(a.part_lse[p0 + (int64_t)sp * a.h] - mx);
+  for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  if (lane == 0) part_den[warp] = den;
+  __syncthreads();
+  den = 0.f;
+  for (int i = 0; i < kThreads / 32; ++i) den += part_den[i];
+  // rounds of up to kThreads columns; the threads left over share the splits
+  for (int c0 = 0; c0 < a.r; c0 += kThreads) {
+    const int nc = min(a.r - c0, kThreads), sl = kThreads / nc, c = tid % nc, si = tid / nc;
+    float o = 0.f;
+    if (si < sl)
+      for (int sp = si; sp < ns; sp += sl) {
+        const int64_t part = p0 + (int64_t)sp * a.h;
+        o = fmaf(expf(a.part_lse[part] - mx), a.part_o[part * a.r + c0 + c], o);
+      }
+    red[tid] = o;
+    __syncthreads();
+    if (tid < nc) {
+      float x = 0.f;
+      for (int i = 0; i < sl; ++i) x += red[i * nc + tid];
+      ol[c0 + tid] = ns == 0 ? 0.f : x / den;
+    }
+    __syncthreads();
+  }
   const T* W = reinterpret_cast<const T*>(a.w_kv_b) + ((int64_t)hh * (a.dn + a.dv) + a.dn) * a.r;
   T* out = reinterpret_cast<T*>(a.o) + ((int64_t)b * a.h + hh) * a.dv;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, nw = blockDim.x / 32;
-  for (int v = warp; v < a.dv; v += nw) {
+  for (int v = warp; v < a.dv; v += kThreads / 32) {
     float acc = 0.f;
     for (int c = lane; c < a.r; c += 32)
       acc = fmaf(Elem<T>::load(W + (int64_t)v * a.r + c), ol[c], acc);
@@ -152,20 +215,25 @@ __global__ void paged_merge_kernel(PagedDecodeArgs a) {
 template <typename T>
 cudaError_t run(const PagedDecodeArgs& a, cudaStream_t st) {
   const dim3 bh(a.B, a.h);
-  paged_absorb_kernel<T><<<bh, 256, a.dn * sizeof(float), st>>>(a);
-  stage_event(1, st);
-  const int smem = paged_simt_smem(a.r + a.dr, a.split_tokens);
-  static std::atomic<uint64_t> set{0};
-  const cudaError_t e = set_dynamic_smem((const void*)paged_split_kernel<T>, kMaxSmem, set);
+  cudaError_t e =
+      launch_pdl(paged_absorb_kernel<T>, bh, dim3(kThreads), a.dn * sizeof(float), st, a);
+  count_launches();
   if (e != cudaSuccess) return e;
-  paged_split_kernel<T><<<dim3(a.B, a.h, a.max_splits), 256, smem, st>>>(a);
+  stage_event(1, st);
+  static std::atomic<uint64_t> set{0}, set_m{0};
+  e = set_dynamic_smem((const void*)paged_split_kernel<T>, kMaxSmem, set);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_split_kernel<T>, dim3(a.B, a.h, a.max_splits), dim3(kThreads),
+                 paged_simt_smem(a.r + a.dr, a.split_tokens), st, a);
+  count_launches();
+  if (e != cudaSuccess) return e;
   stage_event(2, st);
-  static std::atomic<uint64_t> set_m{0};
-  const cudaError_t em = set_dynamic_smem((const void*)paged_merge_kernel<T>, kMaxSmem, set_m);
-  if (em != cudaSuccess) return em;
-  paged_merge_kernel<T><<<bh, 256, a.r * sizeof(float), st>>>(a);
+  e = set_dynamic_smem((const void*)paged_merge_kernel<T>, kMaxSmem, set_m);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_merge_kernel<T>, bh, dim3(kThreads), (a.r + kThreads) * sizeof(float), st, a);
+  count_launches();
+  if (e != cudaSuccess) return e;
   stage_event(3, st);
-  count_launches(3);
   return cudaGetLastError();
 }
 
