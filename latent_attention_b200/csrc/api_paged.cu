@@ -117,11 +117,14 @@ mla_status check_decode(const mla_config& c, bool o_proj, int max_blocks, int bl
 
 }  // namespace
 
+constexpr int64_t kPlanBytes = 4 * (8 + 5 * kMaxRequests);
+
 extern "C" {
 
 size_t mla_paged_workspace_size(int32_t n_blocks) {
   if (n_blocks < 1) return 0;
-  return (size_t)align256(256 + 4 * (((int64_t)n_blocks + 31) / 32));
+  // the status word; then the plan's prefixes or the append's bit per block
+  return (size_t)align256(256 + std::max(kPlanBytes, 4 * (((int64_t)n_blocks + 31) / 32)));
 }
 
 mla_status mla_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t* block_table,
@@ -141,11 +144,11 @@ mla_status mla_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int32_
                         free_state_out, slot_map, positions, cu_new};
   for (const void* p : ptrs)
     if (p && !aligned4(p)) return fail(MLA_ERR_ALIGN, "pointer %p is not 4-byte aligned", p);
-  s = check_workspace(workspace, workspace_bytes, 256);
+  s = check_workspace(workspace, workspace_bytes, 256 + kPlanBytes);
   if (s != MLA_OK) return s;
   mla::PlanArgs a{ctx_len, new_len, block_table, free_ring, free_state, ctx_out, free_state_out,
                   slot_map, positions, cu_new, B, max_blocks, n_blocks, block_size, capacity,
-                  static_cast<uint32_t*>(workspace)};
+                  static_cast<uint32_t*>(workspace), static_cast<int32_t*>(workspace) + 64};
   const cudaError_t e = mla::launch_paged_plan(a, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged plan");
   return mla::succeed();
@@ -167,7 +170,7 @@ mla_status mla_paged_append(const mla_config* cfg, const void* rows, const int32
     return fail(MLA_ERR_ALIGN, "rows or cache is not 16-byte aligned");
   if (!aligned4(slot_map) || !aligned4(scales))
     return fail(MLA_ERR_ALIGN, "slot_map or scales is not 4-byte aligned");
-  const size_t need = mla_paged_workspace_size(n_blocks);
+  const size_t need = 256 + 4 * (((size_t)n_blocks + 31) / 32);
   s = check_workspace(workspace, workspace_bytes, need);
   if (s != MLA_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;

@@ -138,6 +138,7 @@ struct PlanArgs {
   int32_t *ctx_out, *state_out, *slots, *pos, *cu;
   int B, max_blocks, n_blocks, bs, capacity;
   uint32_t* status;
+  int32_t* sums;                   // [8 + 5 B]: the prefixes, where a second grid needs them
 };
 
 // Requests a paged call takes at most: every scan over them fits the shared

@@ -8,9 +8,11 @@
 // a byte is e4m3(byte) * 2^e.  A power of two costs e4m3 nothing (its
 // precision is relative) and makes moving a block to a larger scale an exponent
 // shift: only values that become subnormal are rounded again.
+#include <algorithm>
 #include <climits>
 
 #include "paged.cuh"
+#include "sm100.cuh"
 
 namespace mla {
 namespace {
@@ -24,10 +26,13 @@ using namespace paged;
 // new = -1 gives its held blocks back behind the ring's end.  Blocks given
 // back can be taken from the next call on, so the two never meet.
 //
-// One block of 1024 threads: the three prefix sums over the requests are a
-// scan in registers and shared memory, and the entries that change hands are
-// spread flat over the threads (a binary search in the prefix finds an
-// entry's request), so one long prompt costs no more than many short ones.
+// One block of 1024 threads computes the three prefix sums over the requests,
+// a scan in registers and shared memory.  The entries that change hands and the
+// slot map are spread flat over the threads (a binary search in a prefix finds
+// an entry's request), so one long prompt costs no more than many short ones;
+// many slots are left to a second grid, which finds the prefixes in the
+// workspace.  A new token's block is looked up where it comes from, the old
+// table or the ring, so nothing waits for the table to be written.
 // All or nothing: if anything is out of range or the ring or the slot map is
 // too short, every output says "nothing happened".
 
@@ -40,31 +45,66 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
   return v;
 }
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kFillThreads = 256;
+// One block writes up to this many slots itself (two rounds of its threads).
+constexpr int kPlanOneBlock = 2048;
+
+// What the entries and slots are found from, in shared memory or the workspace.
+struct PlanSums {
+  int32_t *add_end, *give_end, *new_end;   // [B] inclusive prefixes: blocks, blocks, tokens
+  int32_t *held, *after;                   // [B] blocks before, tokens after the step
+  int head, count, ta, tg, tn;             // ring before; blocks taken, given back; new tokens
+};
+__device__ __forceinline__ PlanSums sums_at(int32_t* base, int B) {
+  PlanSums s;
+  s.add_end = base; s.give_end = base + B; s.new_end = base + 2 * B;
+  s.held = base + 3 * B; s.after = base + 4 * B;
+  return s;
+}
 
 __device__ __forceinline__ int wrap(int64_t i, int n) { return (int)(i >= n ? i - n : i); }
 
-__device__ __forceinline__ void write_slot(const PlanArgs& a, int i, int total, const int32_t* ends,
-                                           const int32_t* after) {
-  int slot = -1, at = 0;
-  if (i < total) {
-    const int b = request_of(ends, a.B, i);
-    at = after[b] - (ends[b] - i);               // the request's last new token is after[b] - 1
-    const int blk = a.table[(int64_t)b * a.max_blocks + at / a.bs];
-    if (blk >= 0 && blk < a.n_blocks) slot = blk * a.bs + at % a.bs;
-    else atomicOr(a.status, kStatusBadPage);
+// The step's entries and slots (tn < 0: nothing happened), by threads first,
+// first + step, ...
+__device__ __forceinline__ void fill(const PlanArgs& a, const PlanSums& s, int first, int step) {
+  const int n = a.n_blocks;
+  for (int i = first; i < s.ta; i += step) {
+    const int b = request_of(s.add_end, a.B, i);
+    const int v = a.ring[wrap((int64_t)s.head + i, n)];
+    if (v < 0 || v >= n) atomicOr(a.status, kStatusBadPage);
+    a.table[(int64_t)b * a.max_blocks + s.held[b] + i - (b ? s.add_end[b - 1] : 0)] = v;
   }
-  a.slots[i] = slot;
-  if (a.pos) a.pos[i] = at;
+  for (int i = first; i < s.tg; i += step) {
+    const int b = request_of(s.give_end, a.B, i);
+    const int v = a.table[(int64_t)b * a.max_blocks + i - (b ? s.give_end[b - 1] : 0)];
+    if (v < 0 || v >= n) atomicOr(a.status, kStatusBadPage);
+    a.ring[wrap(wrap((int64_t)s.head + s.count, n) + (int64_t)i, n)] = v;
+  }
+  for (int i = first; i < a.capacity; i += step) {
+    int slot = -1, at = 0;
+    if (i < s.tn) {
+      const int b = request_of(s.new_end, a.B, i);
+      at = s.after[b] - (s.new_end[b] - i);      // the request's last new token is after[b] - 1
+      const int j = at / a.bs, had = s.held[b];
+      const int blk =
+          j < had ? a.table[(int64_t)b * a.max_blocks + j]
+                  : a.ring[wrap((int64_t)s.head + (b ? s.add_end[b - 1] : 0) + j - had, n)];
+      if (blk >= 0 && blk < n) slot = blk * a.bs + at % a.bs;
+      else atomicOr(a.status, kStatusBadPage);
+    }
+    a.slots[i] = slot;
+    if (a.pos) a.pos[i] = at;
+  }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int inline_slots) {
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int alone) {
   extern __shared__ int32_t sm[];
   __shared__ int64_t warp_sum[3][32];
   __shared__ int64_t totals[3];
   __shared__ int32_t s_head, s_count;
-  int32_t *add_end = sm, *give_end = sm + a.B, *new_end = sm + 2 * a.B, *held = sm + 3 * a.B,
-          *after = sm + 4 * a.B;
+  sm100::griddep_wait();
+  sm100::griddep_launch_dependents();
+  PlanSums s = sums_at(alone ? sm : a.sums + 8, a.B);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   if (t == 0) {
     s_head = a.state[0];
@@ -82,12 +122,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int inli
     add += n < 0 ? 0 : wb - hb;
     give += n < 0 ? hb : 0;
     fresh += grow;
-    held[b] = (int)hb;
-    after[b] = n < 0 ? 0 : (int)(c + grow);
+    s.held[b] = (int)hb;
+    s.after[b] = n < 0 ? 0 : (int)(c + grow);
     // inclusive within this thread; the threads before it are added below
-    add_end[b] = (int)add;
-    give_end[b] = (int)give;
-    new_end[b] = (int)fresh;
+    s.add_end[b] = (int)add;
+    s.give_end[b] = (int)give;
+    s.new_end[b] = (int)fresh;
   }
   const int64_t ia = warp_scan(add, lane), ig = warp_scan(give, lane), in = warp_scan(fresh, lane);
   if (lane == 31) {
@@ -96,65 +136,54 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int inli
     warp_sum[2][warp] = in;
   }
   const int any_bad = __syncthreads_or(bad);
-  if (warp == 0) {
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const int64_t v = warp_sum[k][lane], s = warp_scan(v, lane);
-      warp_sum[k][lane] = s - v;
-      if (lane == 31) totals[k] = s;
-    }
+  if (warp < 3) {
+    const int64_t v = warp_sum[warp][lane], x = warp_scan(v, lane);
+    warp_sum[warp][lane] = x - v;
+    if (lane == 31) totals[warp] = x;
   }
   __syncthreads();
   const int64_t ta = totals[0], tg = totals[1], tn = totals[2];
-  const int head = s_head, count = s_count, n = a.n_blocks;
-  const bool broken = any_bad || head < 0 || head >= n || count < 0 || count > n ||
-                      count + tg > n;            // more blocks than the pool has
-  const bool ok = !broken && ta <= count && tn <= a.capacity;
+  const int n = a.n_blocks;
+  s.head = s_head;
+  s.count = s_count;
+  const bool broken = any_bad || s.head < 0 || s.head >= n || s.count < 0 || s.count > n ||
+                      s.count + tg > n;          // more blocks than the pool has
+  const bool ok = !broken && ta <= s.count && tn <= a.capacity;
+  s.ta = ok ? (int)ta : 0;
+  s.tg = ok ? (int)tg : 0;
+  s.tn = ok ? (int)tn : 0;
   // exclusive prefix of this thread's requests (int: used only when ok)
   const int xa = (int)(warp_sum[0][warp] + ia - add), xg = (int)(warp_sum[1][warp] + ig - give),
             xn = (int)(warp_sum[2][warp] + in - fresh);
   for (int b = b0; b < b1; ++b) {
-    add_end[b] += xa;
-    give_end[b] += xg;
-    new_end[b] += xn;
-    a.cu[b + 1] = ok ? new_end[b] : 0;
+    s.add_end[b] += xa;
+    s.give_end[b] += xg;
+    s.new_end[b] += xn;
+    a.cu[b + 1] = ok ? s.new_end[b] : 0;
     const int32_t was = a.ctx[b];                // before ctx_out, which may be ctx
-    a.ctx_out[b] = ok ? after[b] : was;
+    a.ctx_out[b] = ok ? s.after[b] : was;
   }
   if (t == 0) {
     a.cu[0] = 0;
-    a.state_out[0] = ok ? wrap((int64_t)head + ta, n) : head;
-    a.state_out[1] = ok ? (int)(count - ta + tg) : count;
+    a.state_out[0] = ok ? wrap((int64_t)s.head + ta, n) : s.head;
+    a.state_out[1] = ok ? (int)(s.count - ta + tg) : s.count;
     if (!ok) atomicOr(a.status, broken ? kStatusBadPage : kStatusNoBlocks);
+    if (!alone) {
+      a.sums[0] = s.head; a.sums[1] = s.count; a.sums[2] = s.ta; a.sums[3] = s.tg;
+      a.sums[4] = s.tn;
+    }
   }
   __syncthreads();
-  if (ok) {
-    for (int i = t; i < (int)ta; i += kPlanThreads) {
-      const int b = request_of(add_end, a.B, i);
-      const int first = b ? add_end[b - 1] : 0;
-      const int v = a.ring[wrap((int64_t)head + i, n)];
-      if (v < 0 || v >= n) atomicOr(a.status, kStatusBadPage);
-      a.table[(int64_t)b * a.max_blocks + held[b] + i - first] = v;
-    }
-    for (int i = t; i < (int)tg; i += kPlanThreads) {
-      const int b = request_of(give_end, a.B, i);
-      const int first = b ? give_end[b - 1] : 0;
-      const int v = a.table[(int64_t)b * a.max_blocks + i - first];
-      if (v < 0 || v >= n) atomicOr(a.status, kStatusBadPage);
-      a.ring[wrap(wrap((int64_t)head + count, n) + (int64_t)i, n)] = v;
-    }
-  }
-  if (inline_slots) {
-    __syncthreads();
-    for (int i = t; i < a.capacity; i += kPlanThreads)
-      write_slot(a, i, ok ? (int)tn : 0, new_end, after);
-  }
+  if (alone) fill(a, s, t, kPlanThreads);
 }
 
-// The slot map on its own grid, from the plan's cu and lengths.
-__global__ void slots_kernel(PlanArgs a) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < a.capacity) write_slot(a, i, a.cu[a.B], a.cu + 1, a.ctx_out);
+// Entries and slots on their own grid.
+__global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(PlanArgs a) {
+  sm100::griddep_wait();
+  sm100::griddep_launch_dependents();
+  PlanSums s = sums_at(a.sums + 8, a.B);
+  s.head = a.sums[0]; s.count = a.sums[1]; s.ta = a.sums[2]; s.tg = a.sums[3]; s.tn = a.sums[4];
+  fill(a, s, blockIdx.x * kFillThreads + threadIdx.x, gridDim.x * kFillThreads);
 }
 
 // ----------------------------------------------------------------- append
@@ -163,68 +192,83 @@ __global__ void slots_kernel(PlanArgs a) {
 // block; one CTA quantises it:  e = min{e : max|row| <= 448 2^e}; rows of the
 // block in front of the run (offsets below its first slot) are kept and moved
 // to max(e, e_old).  Rows behind the run are dead and stay as they were.
-// A CTA takes the runs that start in its window of the slot map.
+// A CTA takes the runs that start in its window of the slot map, and holds a
+// run's values in registers between the maximum and the rounding (the first
+// kHeld pieces of 16 a thread, 32 rows of 576; longer runs are read again),
+// so that memory sees them once.
 constexpr int kAppendThreads = 256;
+constexpr int kHeld = 5;
 
 template <typename T>
 __global__ void __launch_bounds__(kAppendThreads)
     append_kernel(const T* __restrict__ rows, const int32_t* __restrict__ slots, int n_rows,
                   PagedPool pool, int window, uint32_t* status, uint32_t* claims) {
-  __shared__ int s_count, s_blk, s_off;     // run length (0: no run), its block and first row
+  __shared__ int sl[258];                   // slots w0 - 1 .. w1 + bs - 1
+  __shared__ int starts[128], n_starts;
+  __shared__ int s_len, s_ok;               // run length; the block is this run's
   __shared__ uint32_t s_amax, s_odd;        // largest finite |value|, any NaN or infinity
   const int t = threadIdx.x, W = pool.W, bs = pool.bs;
   const int64_t n_slots = (int64_t)pool.n_blocks * bs;
+  const bool wide = aligned32(rows);        // rows are a multiple of 32 bytes
   const int w0 = blockIdx.x * window, w1 = min(w0 + window, n_rows);
-  for (int i = w0; i < w1; ++i) {
-    __syncthreads();                         // the previous run's shared values are read
-    if (t < 32) {
-      const int s = slots[i], before = i > 0 ? slots[i - 1] : -1;
-      const bool in = s >= 0 && s < n_slots;
-      // a row of the block that the row before it writes: part of that run,
-      // or (not its next slot) refused
-      const bool cont = in && before >= 0 && before / bs == s / bs;
-      if (t == 0) {
-        s_count = 0;
-        s_amax = 0;
-        s_odd = 0;
-        if ((!in && s != -1) || (cont && before + 1 != s)) atomicOr(status, kStatusBadPage);
-      }
-      if (in && !cont) {
-        const int blk = s / bs, off = s % bs, most = min(bs - off, n_rows - i);
-        int cnt = most;
-        for (int k = 0; k < most; k += 32) {
-          const bool same = k + t < most && slots[i + k + t] == s + k + t;
-          const uint32_t m = __ballot_sync(0xffffffffu, same);
-          if (m != 0xffffffffu) { cnt = k + __ffs(~m) - 1; break; }
-        }
-        if (t == 0) {
-          // two runs of one call in one block have no order: the second is refused
-          const uint32_t bit = 1u << (blk & 31);
-          if (atomicOr(&claims[blk >> 5], bit) & bit) {
-            atomicOr(status, kStatusBadPage);
-          } else {
-            s_count = cnt;
-            s_blk = blk;
-            s_off = off;
-          }
-        }
-      }
+  if (t == 0) n_starts = 0;
+  for (int k = t; k < w1 - w0 + bs + 1; k += kAppendThreads) {
+    const int i = w0 - 1 + k;
+    sl[k] = i >= 0 && i < n_rows ? slots[i] : -1;
+  }
+  __syncthreads();
+  if (t < w1 - w0) {
+    const int s = sl[t + 1], before = sl[t];
+    const bool in = s >= 0 && s < n_slots;
+    // a row of the block that the row before it writes: part of that run, or
+    // (not its next slot) refused
+    const bool cont = in && before >= 0 && before / bs == s / bs;
+    if ((!in && s != -1) || (cont && before + 1 != s)) atomicOr(status, kStatusBadPage);
+    if (in && !cont) starts[atomicAdd(&n_starts, 1)] = w0 + t;
+  }
+  __syncthreads();
+  const int todo = n_starts;
+  for (int k = 0; k < todo; ++k) {
+    const int i = starts[k], s = sl[i - w0 + 1], blk = s / bs, off = s % bs;
+    const int most = min(bs - off, n_rows - i);
+    if (t == 0) {
+      s_len = most;
+      s_amax = 0;
+      s_odd = 0;
     }
     __syncthreads();
-    const int cnt = s_count;
-    if (cnt == 0) continue;
-    const int blk = s_blk, off = s_off;
+    if (t < most && sl[i - w0 + 1 + t] != s + t) atomicMin(&s_len, t);
+    __syncthreads();
     const T* src = rows + (int64_t)i * W;
-    const int nv = cnt * W / 16;
-    uint32_t amax = 0, odd = 0;
-    for (int k = t; k < nv; k += kAppendThreads) {
-      float v[16];
-      load16(src + (int64_t)k * 16, v);
+    const int nv = s_len * W / 16;
+    Piece<T> held[kHeld];
 #pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        const uint32_t b = __float_as_uint(v[x]) & 0x7fffffffu;
+    for (int q = 0; q < kHeld; ++q)
+      if (t + q * kAppendThreads < nv) load_piece(src + (t + q * kAppendThreads) * 16, wide, held[q]);
+    if (t == 0) {
+      // two runs of one call in one block have no order: the second is refused
+      const uint32_t bit = 1u << (blk & 31);
+      s_ok = !(atomicOr(&claims[blk >> 5], bit) & bit);
+      if (!s_ok) atomicOr(status, kStatusBadPage);
+    }
+    const float old_scale = off > 0 ? pool.scales[blk] : 1.f;
+    uint32_t amax = 0, odd = 0;
+    auto look = [&](const Piece<T>& x) {
+      float v[16];
+      values(x, v);
+#pragma unroll
+      for (int y = 0; y < 16; ++y) {
+        const uint32_t b = __float_as_uint(v[y]) & 0x7fffffffu;
         if (b < 0x7f800000u) amax = max(amax, b); else odd = 1;
       }
+    };
+#pragma unroll
+    for (int q = 0; q < kHeld; ++q)
+      if (t + q * kAppendThreads < nv) look(held[q]);
+    for (int p = t + kHeld * kAppendThreads; p < nv; p += kAppendThreads) {
+      Piece<T> x;
+      load_piece(src + p * 16, wide, x);
+      look(x);
     }
     amax = __reduce_max_sync(0xffffffffu, amax);
     odd = __reduce_or_sync(0xffffffffu, odd);
@@ -233,45 +277,55 @@ __global__ void __launch_bounds__(kAppendThreads)
       if (odd) atomicOr(&s_odd, 1u);
     }
     __syncthreads();
-    int e = scale_exp(s_amax), e_old = e;
-    uint8_t* base = pool.cache + (int64_t)blk * bs * W;
-    if (off > 0) {
-      if (stored_exp(pool.scales[blk], &e_old)) {
-        e = max(e, e_old);
-      } else {
-        if (t == 0) atomicOr(status, kStatusBadPage);
-        e_old = e;
+    if (s_ok) {
+      int e = scale_exp(s_amax), e_old = e;
+      uint8_t* base = pool.cache + (int64_t)blk * bs * W;
+      if (off > 0) {
+        if (stored_exp(old_scale, &e_old)) {
+          e = max(e, e_old);
+        } else {
+          if (t == 0) atomicOr(status, kStatusBadPage);
+          e_old = e;
+        }
       }
-    }
-    if (e != e_old) {                        // the kept rows move to the larger scale
-      const float f = pow2(e_old - e);
-      uint4* kept = reinterpret_cast<uint4*>(base);
-      for (int k = t; k < off * W / 16; k += kAppendThreads) {
+      if (e != e_old) {                      // the kept rows move to the larger scale
+        const float f = pow2(e_old - e);
+        uint4* kept = reinterpret_cast<uint4*>(base);
+        for (int p = t; p < off * W / 16; p += kAppendThreads) {
+          float v[16];
+          dequant16(kept[p], f, v);
+          kept[p] = make_uint4(to_e4m3x4(v[0], v[1], v[2], v[3]), to_e4m3x4(v[4], v[5], v[6], v[7]),
+                               to_e4m3x4(v[8], v[9], v[10], v[11]),
+                               to_e4m3x4(v[12], v[13], v[14], v[15]));
+        }
+      }
+      const float f = pow2(-e);
+      uint4* dst = reinterpret_cast<uint4*>(base + (int64_t)off * W);
+      const bool any_odd = s_odd != 0;
+      auto put = [&](int p, const Piece<T>& x) {
         float v[16];
-        dequant16(kept[k], f, v);
-        kept[k] = make_uint4(to_e4m3x4(v[0], v[1], v[2], v[3]), to_e4m3x4(v[4], v[5], v[6], v[7]),
-                             to_e4m3x4(v[8], v[9], v[10], v[11]),
-                             to_e4m3x4(v[12], v[13], v[14], v[15]));
-      }
-    }
-    const float f = pow2(-e);
-    uint4* dst = reinterpret_cast<uint4*>(base + (int64_t)off * W);
-    const bool any_odd = s_odd != 0;
-    for (int k = t; k < nv; k += kAppendThreads) {
-      float v[16];
-      load16(src + (int64_t)k * 16, v);
+        values(x, v);
 #pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        // an infinity is stored as NaN, not as 448: x - x is NaN for both
-        if (any_odd) v[x] += v[x] - v[x];
-        v[x] *= f;
+        for (int y = 0; y < 16; ++y) {
+          // an infinity is stored as NaN, not as 448: x - x is NaN for both
+          if (any_odd) v[y] += v[y] - v[y];
+          v[y] *= f;
+        }
+        dst[p] = make_uint4(to_e4m3x4(v[0], v[1], v[2], v[3]), to_e4m3x4(v[4], v[5], v[6], v[7]),
+                            to_e4m3x4(v[8], v[9], v[10], v[11]),
+                            to_e4m3x4(v[12], v[13], v[14], v[15]));
+      };
+#pragma unroll
+      for (int q = 0; q < kHeld; ++q)
+        if (t + q * kAppendThreads < nv) put(t + q * kAppendThreads, held[q]);
+      for (int p = t + kHeld * kAppendThreads; p < nv; p += kAppendThreads) {
+        Piece<T> x;
+        load_piece(src + p * 16, wide, x);
+        put(p, x);
       }
-      dst[k] = make_uint4(to_e4m3x4(v[0], v[1], v[2], v[3]), to_e4m3x4(v[4], v[5], v[6], v[7]),
-                          to_e4m3x4(v[8], v[9], v[10], v[11]),
-                          to_e4m3x4(v[12], v[13], v[14], v[15]));
+      if (t == 0) pool.scales[blk] = pow2(e);
     }
-    __syncthreads();                         // every thread has read the old scale
-    if (t == 0) pool.scales[blk] = pow2(e);
+    __syncthreads();                         // this run's shared values are read
   }
 }
 
@@ -279,9 +333,9 @@ __global__ void __launch_bounds__(kAppendThreads)
 //
 // Rows of all requests back to back, and their prefix sums.  Each CTA scans
 // the lengths into shared memory and takes tiles of kGatherRows rows: the
-// tile's source rows are looked up once, then the tile is a flat list of
-// 16-byte pieces.
-constexpr int kGatherThreads = 256, kGatherRows = 64;
+// tile's source rows are looked up once, then a thread takes one 16-byte
+// column of every R-th row, all its loads in flight before the first is used.
+constexpr int kGatherThreads = 288, kGatherRows = 32, kGatherFly = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(kGatherThreads)
@@ -290,8 +344,8 @@ __global__ void __launch_bounds__(kGatherThreads)
                   int B, int max_blocks, int capacity, uint32_t* status) {
   extern __shared__ int32_t ends[];          // [B] inclusive prefix sums
   __shared__ int64_t warp_sum[kGatherThreads / 32];
-  __shared__ int64_t src[kGatherRows];       // byte offset of the tile's rows, or -1
-  __shared__ float scl[kGatherRows];
+  __shared__ int64_t src[2][kGatherRows];    // byte offset of a tile's rows, or -1
+  __shared__ float scl[2][kGatherRows];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int64_t most = (int64_t)max_blocks * pool.bs;
   const int per = (B + kGatherThreads - 1) / kGatherThreads;
@@ -322,55 +376,78 @@ __global__ void __launch_bounds__(kGatherThreads)
     if (t == 0) cu[0] = 0;
   }
   const int n_rows = min(total, capacity), nv = pool.W / 16;
-  for (int r0 = blockIdx.x * kGatherRows; r0 < n_rows; r0 += gridDim.x * kGatherRows) {
+  // threads of a row, rows at a time; wide rows take several rounds of columns
+  const int tv = min(nv, kGatherThreads), R = kGatherThreads / tv;
+  const int c0 = t % tv, r0 = t / tv;
+  const bool wide = aligned32(rows);
+  auto look_up = [&](int first, int buf) {
     if (t < kGatherRows) {
       int64_t o = -1;
-      if (r0 + t < n_rows) {
-        const int b = request_of(ends, B, r0 + t);
-        const int j = r0 + t - (b ? ends[b - 1] : 0);
+      float s = 0.f;
+      const int i = first + t;
+      if (i < n_rows) {
+        const int b = request_of(ends, B, i);
+        const int j = i - (b ? ends[b - 1] : 0);
         const int blk = table[(int64_t)b * max_blocks + j / pool.bs];
         if (blk >= 0 && blk < pool.n_blocks) {
           o = ((int64_t)blk * pool.bs + j % pool.bs) * pool.W;
-          scl[t] = pool.scales[blk];
+          s = pool.scales[blk];
         } else {
           atomicOr(status, kStatusBadPage);
         }
       }
-      src[t] = o;
+      src[buf][t] = o;
+      scl[buf][t] = s;
     }
-    __syncthreads();
-    const int pieces = min(kGatherRows, n_rows - r0) * nv;
-    for (int k = t; k < pieces; k += kGatherThreads) {
-      const int r = k / nv, c = (k - r * nv) * 16;
-      float v[16];
+  };
+  const int stride = gridDim.x * kGatherRows;
+  int buf = 0;
+  if (blockIdx.x * kGatherRows < n_rows) look_up(blockIdx.x * kGatherRows, 0);
+  for (int first = blockIdx.x * kGatherRows; first < n_rows; first += stride, buf ^= 1) {
+    __syncthreads();                         // the tile's rows are known
+    if (first + stride < n_rows) look_up(first + stride, buf ^ 1);
+    const int here = min(kGatherRows, n_rows - first);
+    if (r0 < R) {
+      for (int c = c0; c < nv; c += tv) {
+        for (int rb = r0; rb < here; rb += R * kGatherFly) {
+          uint4 x[kGatherFly];
 #pragma unroll
-      for (int x = 0; x < 16; ++x) v[x] = 0.f;  // a row whose block is out of range
-      if (src[r] >= 0)
-        dequant16(*reinterpret_cast<const uint4*>(pool.cache + src[r] + c), scl[r], v);
-      store16(rows + (int64_t)(r0 + r) * pool.W + c, v);
+          for (int q = 0; q < kGatherFly; ++q) {
+            const int r = rb + q * R;
+            x[q] = make_uint4(0u, 0u, 0u, 0u);   // a row whose block is out of range
+            if (r < here && src[buf][r] >= 0)
+              x[q] = *reinterpret_cast<const uint4*>(pool.cache + src[buf][r] + c * 16);
+          }
+#pragma unroll
+          for (int q = 0; q < kGatherFly; ++q) {
+            const int r = rb + q * R;
+            if (r >= here) break;
+            float v[16];
+            Piece<T> out;
+            dequant16(x[q], scl[buf][r], v);
+            piece_of(v, out);
+            store_piece(rows + (int64_t)(first + r) * pool.W + c * 16, wide, out);
+          }
+        }
+      }
     }
-    __syncthreads();
   }
 }
-
-// Slots that the planning block writes itself; beyond, a second grid does.
-constexpr int kInlineSlots = 4096;
 
 }  // namespace
 
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
-  const int smem = 5 * 4 * a.B;
   static std::atomic<uint64_t> set{0};
-  cudaError_t e = set_dynamic_smem((const void*)plan_kernel, 5 * 4 * kMaxRequests, set);
+  const cudaError_t e = set_dynamic_smem((const void*)plan_kernel, 5 * 4 * kMaxRequests, set);
   if (e != cudaSuccess) return e;
-  const bool in = a.capacity <= kInlineSlots;
-  plan_kernel<<<1, kPlanThreads, smem, st>>>(a, in);
+  const bool alone = a.capacity <= kPlanOneBlock;
+  const cudaError_t e1 = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads),
+                                    alone ? 5 * 4 * (size_t)a.B : 0, st, a, (int)alone);
   count_launches();
-  if (!in) {
-    slots_kernel<<<(a.capacity + 255) / 256, 256, 0, st>>>(a);
-    count_launches();
-  }
-  return cudaGetLastError();
+  if (e1 != cudaSuccess || alone) return e1;
+  const int grid = std::min((a.capacity + kFillThreads - 1) / kFillThreads, 8 * 148);
+  count_launches();
+  return launch_pdl(plan_fill_kernel, dim3(grid), dim3(kFillThreads), 0, st, a);
 }
 
 cudaError_t launch_paged_append(int dtype, const void* rows, const int32_t* slots, int n_rows,

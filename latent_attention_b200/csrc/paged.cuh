@@ -59,6 +59,23 @@ __device__ __forceinline__ bool stored_exp(float scale, int* e) {
   return (b & 0x807fffffu) == 0 && *e >= kMinExp && *e <= 120;
 }
 
+// 32 bytes at a 32-byte aligned address in one access: a warp's whole sectors,
+// where two accesses of 16 bytes would each touch half of every sector.
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                 "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ bool aligned32(const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
+}
+
 // 16 consecutive elements as floats (16-byte aligned source).
 __device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
 #pragma unroll
@@ -67,34 +84,64 @@ __device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
     v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
   }
 }
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 x = reinterpret_cast<const uint4*>(p)[i];
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
-      v[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-    }
-  }
-}
 __device__ __forceinline__ void store16(float* p, const float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     reinterpret_cast<float4*>(p)[i] =
         make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16]) {
+
+// 16 elements of a row as they lie in memory, 32 or 64 bytes.  wide: the
+// address is 32-byte aligned.
+template <typename T> struct Piece;
+template <> struct Piece<__nv_bfloat16> { static constexpr int N = 8; uint32_t w[8]; };
+template <> struct Piece<float> { static constexpr int N = 16; uint32_t w[16]; };
+
+template <typename T>
+__device__ __forceinline__ void load_piece(const T* p, bool wide, Piece<T>& x) {
+  if (wide) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t w[4];
+    for (int i = 0; i < Piece<T>::N; i += 8) load32(reinterpret_cast<const uint32_t*>(p) + i, x.w + i);
+  } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
-      w[k] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int i = 0; i < Piece<T>::N; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+      x.w[i] = v.x; x.w[i + 1] = v.y; x.w[i + 2] = v.z; x.w[i + 3] = v.w;
     }
-    reinterpret_cast<uint4*>(p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_piece(T* p, bool wide, const Piece<T>& x) {
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < Piece<T>::N; i += 8) store32(reinterpret_cast<uint32_t*>(p) + i, x.w + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < Piece<T>::N; i += 4)
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) =
+          make_uint4(x.w[i], x.w[i + 1], x.w[i + 2], x.w[i + 3]);
+  }
+}
+__device__ __forceinline__ void values(const Piece<float>& x, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(x.w[i]);
+}
+__device__ __forceinline__ void values(const Piece<__nv_bfloat16>& x, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(x.w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(x.w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void piece_of(const float (&v)[16], Piece<float>& x) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x.w[i] = __float_as_uint(v[i]);
+}
+__device__ __forceinline__ void piece_of(const float (&v)[16], Piece<__nv_bfloat16>& x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    x.w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
 }
 

@@ -761,3 +761,38 @@ def test_two_calls_at_once_on_workspaces_of_their_own(cuda):
     torch.cuda.synchronize()
     for out, ref in zip(outs, alone):
         assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_aligned_to_16_bytes_only(cuda, dtype):
+    cfg = bf16(2) if dtype == "bf16" else F32
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    W, bs, n = width(cfg), 32, 100
+    off = 16 // dt.itemsize
+    buf = torch.empty(n * W + off, dtype=dt, device="cuda")
+    rows = buf[off:].view(n, W)
+    assert rows.data_ptr() % 32 == 16
+    host = random_rows(n, W, dt, 3)
+    rows.copy_(host)
+    cache, scales = dirty_pool(6, bs, W, 9)
+    c, s, ws = cache.cuda(), scales.cuda(), paged_ws(6)
+    slots = list(range(5, 5 + n))
+    L.mla_paged_append(cfg, rows, i32(slots), c, s, n, 6, bs, ws)
+    L.mla_check_device_status(ws)
+    want, wsc = O.append(host, slots, cache.numpy(), scales.numpy(), bs)
+    assert np.array_equal(s.cpu().numpy(), wsc)
+    assert np.array_equal(O.E4M3[c.cpu().numpy()], O.E4M3[want])
+    cu = torch.empty(2, dtype=torch.int32, device="cuda")
+    L.mla_paged_gather(cfg, c, s, i32([[0, 1, 2, 3, 4, 5]]), i32([n]), rows, cu, 1, 6, 6, bs, n, ws)
+    L.mla_check_device_status(ws)
+    assert np.array_equal(f64(rows), O.rows_of(want, wsc, [[0, 1, 2, 3, 4, 5]], [n], 0, bs))
+
+
+@pytest.mark.parametrize("capacity", [2048, 2049, 30000])
+def test_plan_on_either_side_of_one_block(cuda, capacity):
+    rng = np.random.default_rng(capacity)
+    ctx = rng.integers(0, 700, 9)
+    new = np.array([capacity // 9] * 8 + [-1])
+    table, ring, state, _ = pool_state(rng, ctx, 16, capacity // 16 + 20, 300)
+    assert check_plan(ctx, new, table, ring, state, 16, capacity, in_place=True)["status"] == "ok"
+    check_plan(ctx, new, table, ring, [state[0], 3], 16, capacity, in_place=True)
