@@ -38,7 +38,7 @@
 // segments with one continuous pipeline.
 //
 // Warps: 0 and 2 TMA of the chunks (a ring of 128-dim boxes; one load per block
-// and box), 2 also the block lookups and L2 prefetch; 1 the segments' queries
+// and box), 2 also the block lookups; 1 the segments' queries
 // and the MMAs of S; 3 the MMAs of PV; from 4 on softmax, groups of 16 (8) heads.  S and
 // PV have a thread each so that neither waits for the other's inputs: PV of a
 // chunk frees the boxes of the next but one.  All waits are bounded; a timeout
@@ -59,7 +59,7 @@ constexpr int R = 512, DR = 64, W = R + DR;
 constexpr int BOX = CT * 128;            // 128 tokens x 128 dims, 16 KB
 constexpr int RBOX = CT * DR;            // 128 tokens x 64 rope dims, 8 KB
 constexpr int GR = 6;                    // lookup ring, chunks
-constexpr int AHEAD = 3;                 // chunks looked up (and prefetched to L2) ahead of loads
+constexpr int AHEAD = 3;                 // chunks looked up ahead of loads
 constexpr float kGrow = 24.f;
 
 // Per head-group size NH (heads of a CTA, padded): ring depth, P buffers and
@@ -537,12 +537,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.g_full[at]);
       sc = 1.f;
-      if (has) {
-        sc = p.scales[id];
-        // the head groups of a unit share the prefetch
-        if (lg > 0 && lane % p.groups == hg)
-          bulk_prefetch_l2(p.cache + (int64_t)id * p.bs * W, (uint32_t)(p.bs * W));
-      }
+      if (has) sc = p.scales[id];
       advance(look);
       id = fetch();
       ++lg;
@@ -551,21 +546,20 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
     int slot = 2;
     uint32_t ph = 1;
     for (int g = 0; !c.done; ++g) {
+      if (c.j == 0) n = p.len[c.s.b];
+      const int valid = min(CT, n - (c.s.c0 + c.j) * CT);
+      const int blocks = (valid + p.bs - 1) >> p.lbs;
       bool ok = true;
-      if (lane == 0) {
-        if (c.j == 0) n = p.len[c.s.b];
-        const int valid = min(CT, n - (c.s.c0 + c.j) * CT);
-        const int blocks = (valid + p.bs - 1) >> p.lbs;
 #pragma unroll 1
-        for (int a = 2; ok && a < 4; ++a) {
-          ok = mbar_wait(&sh.c_empty[slot], ph, abort_v, p.status);
-          if (!ok) break;
-          load_box(a, slot, blocks, sh.ids[g % GR]);
-          slot += a == 2 ? 1 : 3;
-          if (slot >= NS) { slot -= NS; ph ^= 1; }
-        }
+      for (int a = 2; a < 4; ++a) {
+        ok = warp_wait(&sh.c_empty[slot], ph, abort_v, p.status);
+        if (!ok) break;
+        if (elect_one()) load_box(a, slot, blocks, sh.ids[g % GR]);
+        __syncwarp();
+        slot += a == 2 ? 1 : 3;
+        if (slot >= NS) { slot -= NS; ph ^= 1; }
       }
-      if (!__shfl_sync(0xffffffffu, (int)ok, 0)) break;
+      if (!ok) break;
       while (lg <= g + AHEAD && (pending || !look.done)) look_up();
       advance(c);
     }
