@@ -104,7 +104,7 @@ struct Shared {
       r_empty[K::NR], g_full[GR], e_full[GR], s_full[K::NSL], s_free[K::NSL],
       p_full[K::NP], pv_done[K::NP];
   uint32_t tmem_base;
-  int abort_flag, first;
+  int abort_flag;
 };
 template <int NH>
 constexpr int smem_bytes() { return Cfg<NH>::OFF_SH + (int)sizeof(Shared<NH>); }
@@ -115,6 +115,7 @@ static_assert(smem_bytes<64>() <= 227 * 1024 && smem_bytes<48>() <= 227 * 1024 &
 struct AttnParams {
   const int64_t* pre;          // [B + 1] charged chunks
   const int32_t* len;          // [B] tokens
+  const int32_t* first;        // [n_units] sequence at the start of a slice
   const int32_t* table;        // [B, max_blocks]
   const uint8_t* cache;
   const float* scales;
@@ -264,21 +265,6 @@ __device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t
 }
 
 // ------------------------------------------------------------- P2: attention
-// First sequence whose charged chunks reach past r, by a whole warp: every
-// round narrows the range 32-fold.
-__device__ __forceinline__ int seq_at_warp(const int64_t* pre, int B, int64_t r, int lane) {
-  int lo = 0, n = B;                          // the answer is in [lo, lo + n), or B - 1
-  while (n > 1) {
-    const int step = (n + 31) / 32, at = lo + (lane + 1) * step;   // pre[at]: end of `step` sequences
-    const bool past = at >= lo + n || pre[at] > r;
-    const int first = __ffs(__ballot_sync(0xffffffffu, past)) - 1;
-    const int left = lo + n - (lo + first * step);
-    lo += first * step;
-    n = min(step, left);
-  }
-  return min(lo, B - 1);
-}
-
 template <int NH>
 __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -292,16 +278,14 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
   Shared<NH>& sh = *reinterpret_cast<Shared<NH>*>(smem + K::OFF_SH);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int* abort_v = &sh.abort_flag;
-  griddep_wait();
-  griddep_launch_dependents();
   if (smem_u32(smem) & 1023u) {               // the swizzled tiles need it
+    griddep_wait();
     if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
     return;
   }
   const int u = blockIdx.x / p.groups, hg = blockIdx.x % p.groups;
-  const Slice sl = unit_slice(p.pre, p.B, u, p.n_units, p.min_len);
-  if (sl.r0 >= sl.r1) return;
 
+  // what needs nothing of the kernel before this one
   if (warp == 0) {
     if (lane == 0) {
       mbar_init(&sh.q_full, 1);
@@ -334,9 +318,6 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
   } else if (warp == 1) {
     tmem_alloc(&sh.tmem_base, K::TM_COLS);
     tc_fence_before();
-  } else if (warp == 2) {
-    const int b = seq_at_warp(p.pre, p.B, sl.r0, lane);
-    if (lane == 0) sh.first = b;
   } else if (warp == 3 && lane == 0) {
     tma_prefetch(&tmC);
     tma_prefetch(&tmCr);
@@ -353,10 +334,13 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
     tmem_wait_st();
     tc_fence_before();
   }
-  Cursor c;
-  c.start(p.pre, p.B, sl, u, sh.first);
   __syncthreads();
   tc_fence_after();
+  griddep_wait();
+  griddep_launch_dependents();
+  const Slice sl = unit_slice(p.pre, p.B, u, p.n_units, p.min_len);
+  Cursor c;                                   // (done at once where the slice is empty)
+  c.start(p.pre, p.B, sl, u, p.first[u]);
   const auto advance = [&](Cursor& k) { k.next(p.pre, p.B, sl, u); };
 
   // TMA loads of box a of a chunk's `blocks` blocks (ids in shared memory); a
@@ -864,7 +848,8 @@ PagedTcPlan tc_paged_plan(int h, int sms) {
 
 cudaError_t tc_paged_decode(const PagedDecodeArgs& a, cudaStream_t st) {
   const PagedTcPlan& t = a.tc;
-  cudaError_t e = launch_paged_query(a, st);
+  constexpr int kMinLen = 1;                // shortest slice, chunks
+  cudaError_t e = launch_paged_query(a, kMinLen, st);
   if (e != cudaSuccess) return e;
   stage_event(1, st);
   // e4m3 tensors as pairs of bytes: 288 columns of 16 bits
@@ -880,12 +865,12 @@ cudaError_t tc_paged_decode(const PagedDecodeArgs& a, cudaStream_t st) {
       !encode_tmap(&tmCr, a.pool.cache, 2, cdims, str, crbox, 64))
     return cudaErrorInvalidValue;
   AttnParams p{};
-  p.pre = a.pre; p.len = a.len; p.table = a.table;
+  p.pre = a.pre; p.len = a.len; p.first = a.first; p.table = a.table;
   p.cache = a.pool.cache; p.scales = a.pool.scales; p.qf = a.qf;
   p.B = a.B; p.max_blocks = a.max_blocks; p.n_blocks = a.pool.n_blocks; p.bs = a.pool.bs;
   p.lbs = a.pool.bs == 16 ? 4 : a.pool.bs == 32 ? 5 : a.pool.bs == 64 ? 6 : 7;
   p.h = a.h; p.groups = t.groups; p.hg_heads = t.hg_heads;
-  p.n_units = t.n_units; p.min_len = 1;
+  p.n_units = t.n_units; p.min_len = kMinLen;
   p.part_o = a.part_o; p.part_lse = a.part_lse;
   p.o_lat = (float*)a.o_lat;
   p.status = a.status;

@@ -1,5 +1,5 @@
-// The two projections around the tensor-core paged attention, one head and 32
-// sequences a block:
+// The two projections around the tensor-core paged attention, one head and up
+// to 128 sequences a block:
 //
 //   paged_query_kernel   q_lat = W_UK[h]^T q_nope, and [q_lat | q_pe] as two
 //                        e4m3 terms and a power of two; the lengths and the
@@ -8,13 +8,17 @@
 //                        o = W_UV[h] o_lat
 //
 // Both read each head's 128 KB of weights once and do little with them (a
-// decode batch has tens of rows): what bounds them is the time of a launch and
-// of one trip to memory, so the work around the products (rounding to 8 bits,
-// merging) is done where the operands are, and the products are warp-level
-// MMAs on shared memory, whose results the threads hold in registers; a
-// tcgen05 product would have to be read back out of TMEM first.  Neither
-// q_lat nor o_lat is rounded to 16 bits: q_lat goes from fp32 to its two
-// terms, o_lat enters the product as two bf16 terms (16 significant bits).
+// decode batch has tens of rows): what bounds them is the time of a launch, of
+// one trip to memory and of fetching their instructions, so the work around
+// the products (rounding to 8 bits, merging) is done where the operands are,
+// and the products are warp-level MMAs on shared memory, whose results the
+// threads hold in registers; a tcgen05 product would have to be read back out
+// of TMEM first.  (Four blocks a head, in a cluster, took longer: 45 us
+// against 26 at 64 sequences of 128 heads.)  Neither q_lat nor o_lat is rounded
+// to 16 bits: q_lat goes from fp32 to its two terms, o_lat enters the product as
+// two bf16 terms (16 significant bits).
+#include <algorithm>
+
 #include "paged.cuh"
 #include "paged_slices.cuh"
 #include "sm100.cuh"
@@ -28,8 +32,15 @@ using namespace pslices;
 using namespace sm100;
 
 constexpr int R = 512, DR = 64, W = R + DR;
-constexpr int NT = 256;                  // threads, 8 warps
-constexpr int MB = 32;                   // sequences a block
+constexpr int NT = 512;                  // threads, 16 warps
+constexpr int MB = 32;                   // sequences in a round
+
+// Rounds a block: one while the blocks have SMs of their own (the weights are
+// then read by several), more beyond, up to four.
+int rounds_of(const PagedDecodeArgs& a) {
+  const int64_t blocks = (int64_t)a.h * ((a.B + MB - 1) / MB);
+  return (int)std::min<int64_t>(4, (blocks + 147) / 148);
+}
 constexpr int WBOX = 128 * 128;          // 128 rows of 64 bf16 weights
 constexpr int W_BYTES = 8 * WBOX;
 
@@ -66,14 +77,14 @@ struct QueryParams {
   float* qf;                               // [B, groups, NH]
   const int32_t* ctx;
   int64_t* pre;
-  int32_t* len;
-  int B, h, dn, dv, groups, hg_heads, NH;
+  int32_t *len, *first;
+  int B, h, dn, dv, groups, hg_heads, NH, n_units, min_len, rounds;
   int64_t most;                            // tokens a table holds
   float scale_log2;
   uint32_t* status;
 };
-constexpr int Q_STAGE = MB * 2 * W;        // the rows' bytes, both terms
-constexpr int Q_SMEM = W_BYTES + Q_STAGE + 1024;
+constexpr int Q_TILE = MB * 256;           // 32 rows of 128 bf16, two boxes of 64 columns
+constexpr int Q_SMEM = W_BYTES + Q_TILE + 1024;
 
 // Two e4m3 terms of a pair: hi in the low half, lo in the high half.
 __device__ __forceinline__ uint32_t split_pair(float x, float y) {
@@ -126,16 +137,35 @@ __device__ void lengths(const QueryParams& p) {
     p.pre[b + 1] = at;
   }
   if (t == 0) p.pre[0] = 0;
+  __syncthreads();
+  // the sequence at the start of every unit's slice
+  for (int u = t; u < p.n_units; u += NT)
+    p.first[u] = seq_at(p.pre, p.B, unit_slice(p.pre, p.B, u, p.n_units, p.min_len).r0);
+}
+
+// The 16-bit values that the four lanes of a quad hold of each of four groups
+// (v[n]: group n), handed over so that a lane ends with group (lane & 3), in the
+// lanes' order.
+__device__ __forceinline__ uint2 quad_transpose(const uint32_t (&v)[4], int lane) {
+  const uint32_t a = __byte_perm(v[0], v[1], 0x5410), b = __byte_perm(v[2], v[3], 0x5410);
+  const bool up = lane & 2, odd = lane & 1;
+  const uint32_t k = up ? b : a, o = __shfl_xor_sync(0xffffffffu, up ? a : b, 2);
+  const uint32_t lo = __byte_perm(k, o, 0x5410), hi = __byte_perm(k, o, 0x7632);
+  // (this lane, lane ^ 2) and (lane ^ 1, lane ^ 3) of this lane's group
+  const uint32_t x = odd ? hi : lo, y = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+  const uint32_t e = odd ? y : x, f = odd ? x : y;
+  const uint32_t w0 = __byte_perm(e, f, 0x5410), w1 = __byte_perm(e, f, 0x7632);
+  return up ? make_uint2(w1, w0) : make_uint2(w0, w1);
 }
 
 // Block (x, y): x = 0 the lengths, 1 .. h a head, h + 1 the rows that pad the
-// head groups; y: sequences 32 y ...
+// head groups; y: 32 x rounds sequences
 __global__ void __launch_bounds__(NT) paged_query_kernel(const __grid_constant__ CUtensorMap tmW,
                                                          QueryParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full;
   __shared__ int abort_flag;
-  __shared__ uint32_t amax_s[MB][9];
+  __shared__ uint32_t amax_s[2][MB];       // the rows' maxima, of even and odd rounds
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -145,10 +175,11 @@ __global__ void __launch_bounds__(NT) paged_query_kernel(const __grid_constant__
     fence_barrier_init();
     tma_prefetch(&tmW);
   }
+  if (t < 2 * MB) amax_s[t / MB][t % MB] = 0;
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  const int b0 = blockIdx.y * MB, nb = min(MB, p.B - b0);
+  const int b0 = blockIdx.y * MB * p.rounds, nb = min(MB * p.rounds, p.B - b0);
   if (blockIdx.x == 0) {
     if (blockIdx.y == 0) lengths(p);
     return;
@@ -173,131 +204,121 @@ __global__ void __launch_bounds__(NT) paged_query_kernel(const __grid_constant__
     return;
   }
   const int hh = blockIdx.x - 1;
-  const uint32_t wbase = smem_u32(smem);
-  float acc[2][8][4];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[m][n][k] = 0.f;
-  const int r = lane >> 2, kq = 2 * (lane & 3);
-  bool ok = true;
-  for (int kc = 0; kc < p.dn; kc += 128) {
-    // 128 rows of W_UK[h]; past dn they are W_UV's and meet zeros of q
-    if (t == 0) {
-      mbar_arrive_expect_tx(&full, W_BYTES);
-      for (int i = 0; i < 8; ++i)
-        tma_load_2d(smem + i * WBOX, &tmW, 64 * i, hh * (p.dn + p.dv) + kc, &full);
-    }
-    uint32_t a[2][8][4];
+  const int g = hh / p.hg_heads, i = hh % p.hg_heads;
+  const uint32_t wbase = smem_u32(smem), qbase = wbase + W_BYTES;
+  const int r = lane >> 2;
+  // a 16-byte piece of q_nope and four values of q_pe a thread
+  const int rr = t >> 4, part = t & 15;
+  int phase = 0;
+  for (int round = 0; round * MB < nb; ++round) {
+    const int base = b0 + round * MB, n = min(MB, nb - round * MB);
+    float acc[2][4][4];                    // 32 rows x this warp's 32 dims
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int row = m * 16 + r + (q & 1) * 8, k = kc + ks * 16 + kq + (q >> 1) * 8;
-          a[m][ks][q] =
-              row < nb && k < p.dn
-                  ? *reinterpret_cast<const uint32_t*>(
-                        p.q_nope + ((int64_t)(b0 + row) * p.h + hh) * p.dn + k)
-                  : 0u;
-        }
-    if (!mbar_wait(&full, (kc >> 7) & 1, &abort_flag, p.status)) { ok = false; break; }
-    // this warp's 64 latent columns are one box
+        for (int k = 0; k < 4; ++k) acc[m][q][k] = 0.f;
+    uint2 pe2 = make_uint2(0u, 0u);
+    if (rr < n)
+      pe2 = reinterpret_cast<const uint2*>(p.q_pe + ((int64_t)(base + rr) * p.h + hh) * DR)[part];
+    for (int kc = 0; kc < p.dn; kc += 128) {
+      // 128 rows of W_UK[h]; past dn they are W_UV's and meet zeros of q.  Up
+      // to 128 rows they stay for all rounds.
+      const bool load = round == 0 || p.dn > 128;
+      if (t == 0 && load) {
+        mbar_arrive_expect_tx(&full, W_BYTES);
+        for (int x = 0; x < 8; ++x)
+          tma_load_2d(smem + x * WBOX, &tmW, 64 * x, hh * (p.dn + p.dv) + kc, &full);
+      }
+      uint4 q4 = make_uint4(0u, 0u, 0u, 0u);
+      if (rr < n && kc + 8 * part < p.dn)
+        q4 = *reinterpret_cast<const uint4*>(p.q_nope + ((int64_t)(base + rr) * p.h + hh) * p.dn +
+                                             kc + 8 * part);
+      st_shared_v4(qbase + (part >> 3) * (Q_TILE / 2) + box_at(rr, part & 7), q4.x, q4.y, q4.z,
+                   q4.w);
+      __syncthreads();
+      // (after a timeout the block goes on; the status word says so)
+      if (load) mbar_wait(&full, phase++ & 1, &abort_flag, p.status);
+#pragma unroll 2
+      for (int ks = 0; ks < 8; ++ks) {
+        uint32_t a[2][4], b[2][4];
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
+        for (int m = 0; m < 2; ++m)
+          ldsm4(qbase + (ks >> 2) * (Q_TILE / 2) +
+                    box_at(m * 16 + (lane & 15), 2 * (ks & 3) + (lane >> 4)), a[m]);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        uint32_t b[4];
-        ldsm4_t(wbase + warp * WBOX + box_at(ks * 16 + (lane & 15), 2 * n + (lane >> 4)), b);
+        for (int q = 0; q < 2; ++q)
+          ldsm4_t(wbase + (warp >> 1) * WBOX +
+                      box_at(ks * 16 + (lane & 15), 4 * (warp & 1) + 2 * q + (lane >> 4)), b[q]);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if (m * 16 >= nb) continue;
-          mma16816(acc[m][2 * n], a[m][ks], b[0], b[1]);
-          mma16816(acc[m][2 * n + 1], a[m][ks], b[2], b[3]);
-        }
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            mma16816(acc[m][2 * q], a[m], b[q][0], b[q][1]);
+            mma16816(acc[m][2 * q + 1], a[m], b[q][2], b[q][3]);
+          }
+      }
+      __syncthreads();                     // weights and q are read
+    }
+    // the rows' maxima
+    uint32_t* amax = amax_s[round & 1];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t y = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          y = max(y, max(finite_bits(acc[m][q][2 * half]), finite_bits(acc[m][q][2 * half + 1])));
+        y = max(y, __shfl_xor_sync(0xffffffffu, y, 1));
+        y = max(y, __shfl_xor_sync(0xffffffffu, y, 2));
+        if ((lane & 3) == 0) atomicMax(&amax[m * 16 + half * 8 + r], y);
+      }
+    float pe[4] = {__uint_as_float(pe2.x << 16), __uint_as_float(pe2.x & 0xffff0000u),
+                   __uint_as_float(pe2.y << 16), __uint_as_float(pe2.y & 0xffff0000u)};
+    {
+      uint32_t y = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y = max(y, finite_bits(pe[k]));
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) y = max(y, __shfl_xor_sync(0xffffffffu, y, o));
+      if (part == 0) atomicMax(&amax[rr], y);
+    }
+    __syncthreads();
+    if (t < MB) amax_s[~round & 1][t] = 0;  // for the next round (its barriers lie between)
+#pragma unroll 1
+    for (int mh = 0; mh < 4; ++mh) {
+      const int row = (mh >> 1) * 16 + (mh & 1) * 8 + r;
+      const float f = pow2(-scale_exp(amax[row]));
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float x, y;
+        x = mh == 0 ? acc[0][q][0] : mh == 1 ? acc[0][q][2] : mh == 2 ? acc[1][q][0] : acc[1][q][2];
+        y = mh == 0 ? acc[0][q][1] : mh == 1 ? acc[0][q][3] : mh == 2 ? acc[1][q][1] : acc[1][q][3];
+        const uint32_t v = split_pair(x * f, y * f);
+        hi[q] = v & 0xffffu;
+        lo[q] = v >> 16;
+      }
+      const uint2 h2 = quad_transpose(hi, lane), l2 = quad_transpose(lo, lane);
+      if (row < n) {
+        uint8_t* dst = p.q8 + (((int64_t)(base + row) * p.groups + g) * 2 * p.NH + i) * W +
+                       warp * 32 + 8 * (lane & 3);
+        *reinterpret_cast<uint2*>(dst) = h2;
+        *reinterpret_cast<uint2*>(dst + (int64_t)p.NH * W) = l2;
       }
     }
-    __syncthreads();                       // the weights are read
-  }
-  if (!ok) return;                         // the status word says so
-  // the rows' maxima
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t x = 0;
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-        x = max(x, max(finite_bits(acc[m][n][2 * half]), finite_bits(acc[m][n][2 * half + 1])));
-      x = max(x, __shfl_xor_sync(0xffffffffu, x, 1));
-      x = max(x, __shfl_xor_sync(0xffffffffu, x, 2));
-      if ((lane & 3) == 0) amax_s[m * 16 + half * 8 + r][warp] = x;
+    if (rr < n) {
+      const int e = scale_exp(amax[rr]);
+      const float f = pow2(-e);
+      const uint32_t v0 = split_pair(pe[0] * f, pe[1] * f), v1 = split_pair(pe[2] * f, pe[3] * f);
+      const int64_t bg = (int64_t)(base + rr) * p.groups + g;
+      uint8_t* dst = p.q8 + (bg * 2 * p.NH + i) * W + R + 4 * part;
+      *reinterpret_cast<uint32_t*>(dst) = __byte_perm(v0, v1, 0x5410);
+      *reinterpret_cast<uint32_t*>(dst + (int64_t)p.NH * W) = __byte_perm(v0, v1, 0x7632);
+      if (part == 0) p.qf[bg * p.NH + i] = p.scale_log2 * pow2(e);
     }
-  const int rr = t >> 3, part = t & 7;     // eight threads a row for its rope part
-  float pe[8];
-  {
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (rr < nb)
-      x = reinterpret_cast<const uint4*>(p.q_pe + ((int64_t)(b0 + rr) * p.h + hh) * DR)[part];
-    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      pe[2 * i] = __uint_as_float(xw[i] << 16);
-      pe[2 * i + 1] = __uint_as_float(xw[i] & 0xffff0000u);
-      m = max(m, max(finite_bits(pe[2 * i]), finite_bits(pe[2 * i + 1])));
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (part == 0) amax_s[rr][8] = m;
-  }
-  __syncthreads();
-  auto exponent = [&](int row) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 9; ++i) m = max(m, amax_s[row][i]);
-    return scale_exp(m);
-  };
-  uint8_t* stage = smem + W_BYTES;         // [MB][2][W]
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int row = m * 16 + half * 8 + r;
-      const float f = pow2(-exponent(row));
-      uint8_t* dst = stage + row * 2 * W + warp * 64 + kq;
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const uint32_t v = split_pair(acc[m][n][2 * half] * f, acc[m][n][2 * half + 1] * f);
-        *reinterpret_cast<uint16_t*>(dst + 8 * n) = (uint16_t)v;
-        *reinterpret_cast<uint16_t*>(dst + W + 8 * n) = (uint16_t)(v >> 16);
-      }
-    }
-  const int g = hh / p.hg_heads, i = hh % p.hg_heads;
-  {
-    const int e = exponent(rr);
-    const float f = pow2(-e);
-    uint32_t v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = split_pair(pe[2 * k] * f, pe[2 * k + 1] * f);
-    uint8_t* dst = stage + rr * 2 * W + R + part * 8;
-    *reinterpret_cast<uint2*>(dst) = make_uint2((v[0] & 0xffffu) | (v[1] << 16),
-                                                (v[2] & 0xffffu) | (v[3] << 16));
-    *reinterpret_cast<uint2*>(dst + W) = make_uint2((v[0] >> 16) | (v[1] & 0xffff0000u),
-                                                    (v[2] >> 16) | (v[3] & 0xffff0000u));
-    if (part == 0 && rr < nb)
-      p.qf[((int64_t)(b0 + rr) * p.groups + g) * p.NH + i] = p.scale_log2 * pow2(e);
-  }
-  __syncthreads();
-  for (int k = t; k < nb * 2 * (W / 16); k += NT) {
-    const int row = k / (2 * (W / 16)), rest = k % (2 * (W / 16));
-    const int term = rest / (W / 16), c = rest % (W / 16);
-    const int64_t bg = (int64_t)(b0 + row) * p.groups + g;
-    *reinterpret_cast<uint4*>(p.q8 + ((bg * 2 + term) * p.NH + i) * W + c * 16) =
-        *reinterpret_cast<const uint4*>(stage + (row * 2 + term) * W + c * 16);
   }
 }
 
@@ -307,14 +328,16 @@ struct OutputParams {
   const float* o_lat;                      // [B, h, R]: sequences in one segment
   const int64_t* pre;
   __nv_bfloat16* out;                      // [B, h, dv]
-  int B, h, dn, dv, n_units, min_len;
+  int B, h, dn, dv, n_units, min_len, rounds;
   uint32_t* status;
 };
-constexpr int A_BYTES = 8 * MB * 128;      // o_lat of the block's sequences, one bf16 term
-constexpr int O_RED = 8 * R * 4;
-constexpr int O_SMEM = W_BYTES + 2 * A_BYTES + O_RED + 1024;
-constexpr int kUnits = 512;               // most units (host side: tc_paged_plan)
-constexpr int kShared = 4;                 // more partials than this: the whole block merges
+constexpr int A_BYTES = 8 * MB * 128;      // o_lat of 32 sequences, one bf16 term
+constexpr int PS = 132;                    // floats of a row of the sums (128, padded)
+constexpr int O_SUMS = MB * PS * 4;        // (also 8 rows of 512: the merge of many partials)
+static_assert(O_SUMS >= 8 * R * 4, "sums");
+constexpr int O_SMEM = W_BYTES + 2 * A_BYTES + O_SUMS + 1024;
+constexpr int kUnits = 512;                // most units (host side: tc_paged_plan)
+constexpr int kShared = 8;                 // more partials than this: the whole block merges
 
 __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant__ CUtensorMap tmW,
                                                           OutputParams p) {
@@ -322,157 +345,186 @@ __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant_
   __shared__ __align__(8) uint64_t full;
   __shared__ int abort_flag;
   __shared__ uint32_t many;                // rows that the whole block merges
-  __shared__ float w_s[2 * kUnits];        // lse and weights of one such row's partials
+  __shared__ const float* src_s[MB][kShared];   // a row's partials
+  __shared__ float w_s[MB][kShared];       // and their weights
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int hh = blockIdx.x, b0 = blockIdx.y * MB, nb = min(MB, p.B - b0);
+  const int hh = blockIdx.x;
+  const int b0 = blockIdx.y * MB * p.rounds, nb = min(MB * p.rounds, p.B - b0);
   const uint32_t wbase = smem_u32(smem), abase = wbase + W_BYTES;
-  float* red = reinterpret_cast<float*>(smem + W_BYTES + 2 * A_BYTES);
+  float* sums = reinterpret_cast<float*>(smem + W_BYTES + 2 * A_BYTES);
+  __shared__ float u_s[2 * kUnits];        // lse and weights of one row with many partials
+  auto load_w = [&](int nc) {
+    mbar_arrive_expect_tx(&full, W_BYTES);
+    for (int i = 0; i < 8; ++i)
+      tma_load_2d(smem + i * WBOX, &tmW, 64 * i, hh * (p.dn + p.dv) + p.dn + nc, &full);
+  };
   if (t == 0) {
     mbar_init(&full, 1);
     abort_flag = 0;
-    many = 0;
     fence_barrier_init();
     // The weights do not depend on the kernel before this one (which started
     // only once all before it had finished): they are on their way while it
     // ends.
-    mbar_arrive_expect_tx(&full, W_BYTES);
-    for (int i = 0; i < 8; ++i)
-      tma_load_2d(smem + i * WBOX, &tmW, 64 * i, hh * (p.dn + p.dv) + p.dn, &full);
+    load_w(0);
   }
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
 
-  // 16 dims of a row as two bf16 terms into the A operand's boxes
-  auto put = [&](int row, int at16, const float (&v)[16]) {
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      hi[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-      lo[i] = pack_bf16(v[2 * i] - __uint_as_float(hi[i] << 16),
-                        v[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u));
-    }
-    const uint32_t box = abase + (at16 >> 2) * MB * 128;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint32_t at = box + box_at(row, 2 * (at16 & 3) + q);
-      st_shared_v4(at, hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-      st_shared_v4(at + A_BYTES, lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
-    }
+  // four dims of a row as two bf16 terms into the A operand's boxes
+  auto put = [&](int row, int d, const float4& v) {
+    const uint32_t h0 = pack_bf16(v.x, v.y), h1 = pack_bf16(v.z, v.w);
+    const uint32_t l0 = pack_bf16(v.x - __uint_as_float(h0 << 16),
+                                  v.y - __uint_as_float(h0 & 0xffff0000u));
+    const uint32_t l1 = pack_bf16(v.z - __uint_as_float(h1 << 16),
+                                  v.w - __uint_as_float(h1 & 0xffff0000u));
+    uint8_t* at = smem + W_BYTES + (d >> 6) * MB * 128 + box_at(row, (d & 63) >> 3) + (d & 7) * 2;
+    *reinterpret_cast<uint2*>(at) = make_uint2(h0, h1);
+    *reinterpret_cast<uint2*>(at + A_BYTES) = make_uint2(l0, l1);
   };
-  for (int row = warp; row < MB; row += NT / 32) {
-    float v[16];
+  int phase = 0;
+  bool coming = true;                      // weights are on their way
+  for (int round = 0; round * MB < nb; ++round) {
+    const int base = b0 + round * MB, n = min(MB, nb - round * MB);
+    if (t == 0) many = 0;
+    __syncthreads();
+    // a thread per row: where its partial results lie, and their weights
+    if (t < MB) {
+      const int b = base + t;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    const int b = b0 + row;
-    if (row < nb && p.pre[b + 1] != p.pre[b]) {
-      const SeqUnits su = seq_units(p.pre, b, p.B, p.n_units, p.min_len);
-      if (su.u0 == su.u1) {
-        load16(p.o_lat + ((int64_t)b * p.h + hh) * R + lane * 16, v);
-      } else if (su.u1 - su.u0 < kShared) {
-        float mx = -INFINITY, den = 0.f, lse[kShared];
+      for (int i = 0; i < kShared; ++i) src_s[t][i] = nullptr;
+      if (t < n && p.pre[b + 1] != p.pre[b]) {
+        const SeqUnits su = seq_units(p.pre, b, p.B, p.n_units, p.min_len);
+        if (su.u0 == su.u1) {
+          src_s[t][0] = p.o_lat + ((int64_t)b * p.h + hh) * R;
+          w_s[t][0] = 1.f;
+        } else if (su.u1 - su.u0 < kShared) {
+          float mx = -INFINITY, den = 0.f, lse[kShared];
 #pragma unroll
-        for (int i = 0; i < kShared; ++i) {
-          lse[i] = su.u0 + i <= su.u1
-                       ? p.part_lse[(int64_t)seq_slot(su, su.u0 + i) * p.h + hh] : -INFINITY;
-          mx = fmaxf(mx, lse[i]);
+          for (int i = 0; i < kShared; ++i) {
+            lse[i] = su.u0 + i <= su.u1
+                         ? p.part_lse[(int64_t)seq_slot(su, su.u0 + i) * p.h + hh] : -INFINITY;
+            mx = fmaxf(mx, lse[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < kShared; ++i) {
+            lse[i] = su.u0 + i <= su.u1 ? exp2f(lse[i] - mx) : 0.f;
+            den += lse[i];
+          }
+#pragma unroll
+          for (int i = 0; i < kShared; ++i)
+            if (su.u0 + i <= su.u1) {
+              src_s[t][i] = p.part_o + ((int64_t)seq_slot(su, su.u0 + i) * p.h + hh) * R;
+              w_s[t][i] = lse[i] / den;
+            }
+        } else {
+          atomicOr(&many, 1u << t);
         }
+      }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int row = warp; row < MB; row += NT / 32) {
+      float4 v[4];
+      const float* src = src_s[row][0];
 #pragma unroll
-        for (int i = 0; i < kShared; ++i) {
-          if (su.u0 + i > su.u1) break;
-          const float w = exp2f(lse[i] - mx);
-          float x[16];
-          load16(p.part_o + ((int64_t)seq_slot(su, su.u0 + i) * p.h + hh) * R + lane * 16, x);
-          den += w;
+      for (int q = 0; q < 4; ++q) v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int i = 0; src; src = ++i < kShared ? src_s[row][i] : nullptr) {
+        const float w = w_s[row][i];
+        float4 x[4];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = fmaf(w, x[k], v[k]);
+        for (int q = 0; q < 4; ++q) x[q] = reinterpret_cast<const float4*>(src)[lane + 32 * q];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[q].x = fmaf(w, x[q].x, v[q].x); v[q].y = fmaf(w, x[q].y, v[q].y);
+          v[q].z = fmaf(w, x[q].z, v[q].z); v[q].w = fmaf(w, x[q].w, v[q].w);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) put(row, 4 * lane + 128 * q, v[q]);
+    }
+    for (uint32_t left = many; left; left &= left - 1) {
+      const int row = __ffs(left) - 1, b = base + row;
+      const SeqUnits su = seq_units(p.pre, b, p.B, p.n_units, p.min_len);
+      const int nu = su.u1 - su.u0 + 1;    // at most kUnits
+      float mx = -INFINITY, den = 0.f;
+      __syncthreads();
+      for (int i = t; i < nu; i += NT)
+        u_s[i] = p.part_lse[(int64_t)seq_slot(su, su.u0 + i) * p.h + hh];
+      __syncthreads();
+      for (int i = lane; i < nu; i += 32) mx = fmaxf(mx, u_s[i]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      for (int i = t; i < nu; i += NT) u_s[kUnits + i] = exp2f(u_s[i] - mx);
+      __syncthreads();
+      // every eighth partial and half of the dims a warp
+      float4 v[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int at = lane + 64 * (warp >> 3);
+#pragma unroll 4
+      for (int i = warp & 7; i < nu; i += 8) {
+        const float4* src = reinterpret_cast<const float4*>(
+            p.part_o + ((int64_t)seq_slot(su, su.u0 + i) * p.h + hh) * R);
+        const float w = u_s[kUnits + i];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float4 x = src[at + 32 * q];
+          v[q].x = fmaf(w, x.x, v[q].x); v[q].y = fmaf(w, x.y, v[q].y);
+          v[q].z = fmaf(w, x.z, v[q].z); v[q].w = fmaf(w, x.w, v[q].w);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        reinterpret_cast<float4*>(sums + (warp & 7) * R)[at + 32 * q] = v[q];
+      for (int i = lane; i < nu; i += 32) den += u_s[kUnits + i];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+      __syncthreads();
+      if (t < R / 4) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < 8; ++w) {
+          const float4 x = reinterpret_cast<const float4*>(sums + w * R)[t];
+          y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
         }
         const float inv = 1.f / den;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] *= inv;
-      } else {
-        if (lane == 0) atomicOr(&many, 1u << row);
-        continue;
+        y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
+        put(row, 4 * t, y);
       }
     }
-    put(row, lane, v);
-  }
-  __syncthreads();
-  for (uint32_t left = many; left; left &= left - 1) {
-    const int row = __ffs(left) - 1, b = b0 + row;
-    const SeqUnits su = seq_units(p.pre, b, p.B, p.n_units, p.min_len);
-    const int n = su.u1 - su.u0 + 1;       // at most kUnits
-    float mx = -INFINITY;
-    for (int i = lane; i < n; i += 32) {
-      const float x = p.part_lse[(int64_t)seq_slot(su, su.u0 + i) * p.h + hh];
-      if (warp == 0) w_s[i] = x;
-      mx = fmaxf(mx, x);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     __syncthreads();
-    for (int i = t; i < n; i += NT) w_s[kUnits + i] = exp2f(w_s[i] - mx);
-    __syncthreads();
-    float v[16], den = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = 0.f;
-#pragma unroll 2
-    for (int i = warp; i < n; i += NT / 32) {
-      float x[16];
-      load16(p.part_o + ((int64_t)seq_slot(su, su.u0 + i) * p.h + hh) * R + lane * 16, x);
-      const float w = w_s[kUnits + i];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] = fmaf(w, x[k], v[k]);
-    }
-    store16(red + warp * R + lane * 16, v);
-    for (int i = lane; i < n; i += 32) den += w_s[kUnits + i];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    __syncthreads();
-    if (warp == 0) {
-      const float inv = 1.f / den;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] = 0.f;
-      for (int w = 0; w < NT / 32; ++w) {
-        float x[16];
-        load16(red + w * R + lane * 16, x);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] += x[k];
+    // up to 128 output columns the weights stay for all rounds
+    for (int nc = 0; nc < p.dv; nc += 128) {
+      if (!coming && p.dv > 128) {
+        if (t == 0) load_w(nc);
+        coming = true;
       }
-#pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] *= inv;
-      put(row, lane, v);
-    }
-    __syncthreads();
-  }
-  for (int nc = 0; nc < p.dv; nc += 128) {
-    if (nc > 0 && t == 0) {
-      mbar_arrive_expect_tx(&full, W_BYTES);
-      for (int i = 0; i < 8; ++i)
-        tma_load_2d(smem + i * WBOX, &tmW, 64 * i, hh * (p.dn + p.dv) + p.dn + nc, &full);
-    }
-    if (!mbar_wait(&full, (nc >> 7) & 1, &abort_flag, p.status)) return;
-    const int n0 = warp * 16;              // this warp's rows of W_UV
-    if (nc + n0 < p.dv) {
+      // (after a timeout the block goes on; the status word says so)
+      if (coming) mbar_wait(&full, phase++ & 1, &abort_flag, p.status);
+      coming = false;
+      // a warp: 16 columns, half of the dims
+      const int n0 = (warp & 7) * 16, kh = warp >> 3;
       float acc[2][2][4];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[m][n][k] = 0.f;
-#pragma unroll 4
-      for (int ks = 0; ks < R / 16; ++ks) {
+          for (int k = 0; k < 4; ++k) acc[m][q][k] = 0.f;
+#pragma unroll 2
+      for (int ks = 16 * kh; ks < 16 * kh + 16; ++ks) {
         const int box = ks >> 2, c = 2 * (ks & 3);
         uint32_t b[4];
         ldsm4(wbase + box * WBOX +
                   box_at(n0 + (lane & 7) + ((lane >> 4) & 1) * 8, c + ((lane >> 3) & 1)), b);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          if (m * 16 >= nb) continue;
-          const uint32_t at = abase + box * MB * 128 + box_at(m * 16 + (lane & 15), c + (lane >> 4));
+          if (m * 16 >= n) continue;
+          const uint32_t at =
+              abase + box * MB * 128 + box_at(m * 16 + (lane & 15), c + (lane >> 4));
           uint32_t hi[4], lo[4];
           ldsm4(at, hi);
           ldsm4(at + A_BYTES, lo);
@@ -482,20 +534,38 @@ __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant_
           mma16816(acc[m][1], hi, b[2], b[3]);
         }
       }
+      // the second half's sums to the first
+      float* const at = sums + (lane >> 2) * PS + n0 + 2 * (lane & 3);
+      if (kh == 1) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int row = m * 16 + half * 8 + (lane >> 2);
-            const int col = nc + n0 + n * 8 + 2 * (lane & 3);
-            if (row < nb && col < p.dv)
-              *reinterpret_cast<uint32_t*>(p.out + ((int64_t)(b0 + row) * p.h + hh) * p.dv + col) =
-                  pack_bf16(acc[m][n][2 * half], acc[m][n][2 * half + 1]);
-          }
+            for (int half = 0; half < 2; ++half)
+              *reinterpret_cast<float2*>(at + (m * 16 + half * 8) * PS + q * 8) =
+                  make_float2(acc[m][q][2 * half], acc[m][q][2 * half + 1]);
+      }
+      __syncthreads();
+      if (kh == 0) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int row = m * 16 + half * 8 + (lane >> 2);
+              const int col = nc + n0 + q * 8 + 2 * (lane & 3);
+              const float2 x =
+                  *reinterpret_cast<const float2*>(at + (m * 16 + half * 8) * PS + q * 8);
+              if (row < n && col < p.dv)
+                *reinterpret_cast<uint32_t*>(p.out + ((int64_t)(base + row) * p.h + hh) * p.dv +
+                                             col) =
+                    pack_bf16(acc[m][q][2 * half] + x.x, acc[m][q][2 * half + 1] + x.y);
+            }
+      }
+      __syncthreads();                     // sums and, past 128 columns, weights are read
     }
-    __syncthreads();                       // the weights are read
   }
 }
 
@@ -508,7 +578,7 @@ bool weight_map(CUtensorMap* m, const PagedDecodeArgs& a) {
 
 }  // namespace
 
-cudaError_t launch_paged_query(const PagedDecodeArgs& a, cudaStream_t st) {
+cudaError_t launch_paged_query(const PagedDecodeArgs& a, int min_len, cudaStream_t st) {
   CUtensorMap tmW;
   if (!weight_map(&tmW, a)) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> set{0};
@@ -520,12 +590,15 @@ cudaError_t launch_paged_query(const PagedDecodeArgs& a, cudaStream_t st) {
   q.q8 = a.q8; q.qf = a.qf; q.ctx = a.ctx; q.pre = a.pre; q.len = a.len;
   q.B = a.B; q.h = a.h; q.dn = a.dn; q.dv = a.dv;
   q.groups = a.tc.groups; q.hg_heads = a.tc.hg_heads; q.NH = a.tc.NH;
+  q.first = a.first; q.n_units = a.tc.n_units; q.min_len = min_len;
   q.most = (int64_t)a.max_blocks * a.pool.bs;
   q.scale_log2 = a.scale * 1.4426950408889634f;
   q.status = a.status;
+  q.rounds = rounds_of(a);
   const bool pads = q.groups * q.NH > q.h;
   count_launches();
-  return launch_pdl(paged_query_kernel, dim3(1 + a.h + pads, (a.B + MB - 1) / MB), dim3(NT), Q_SMEM,
+  return launch_pdl(paged_query_kernel, dim3(1 + a.h + pads, (a.B + MB * q.rounds - 1) / (MB * q.rounds)), dim3(NT),
+                    Q_SMEM,
                     st, tmW, q);
 }
 
@@ -540,9 +613,10 @@ cudaError_t launch_paged_output(const PagedDecodeArgs& a, int min_len, cudaStrea
   o.out = (__nv_bfloat16*)a.o;
   o.B = a.B; o.h = a.h; o.dn = a.dn; o.dv = a.dv; o.n_units = a.tc.n_units; o.min_len = min_len;
   o.status = a.status;
+  o.rounds = rounds_of(a);
   count_launches();
-  return launch_pdl(paged_output_kernel, dim3(a.h, (a.B + MB - 1) / MB), dim3(NT), O_SMEM, st, tmW,
-                    o);
+  return launch_pdl(paged_output_kernel, dim3(a.h, (a.B + MB * o.rounds - 1) / (MB * o.rounds)), dim3(NT),
+                    O_SMEM, st, tmW, o);
 }
 
 }  // namespace mla

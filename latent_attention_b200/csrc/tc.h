@@ -24,7 +24,7 @@ bool tc_paged_supported(const mla_config& c);
 PagedTcPlan tc_paged_plan(int h, int sms);
 cudaError_t tc_paged_decode(const PagedDecodeArgs& a, cudaStream_t st);
 // Its projections: query (and lengths, status word), output.
-cudaError_t launch_paged_query(const PagedDecodeArgs& a, cudaStream_t st);
+cudaError_t launch_paged_query(const PagedDecodeArgs& a, int min_len, cudaStream_t st);
 cudaError_t launch_paged_output(const PagedDecodeArgs& a, int min_len, cudaStream_t st);
 
 }  // namespace mla

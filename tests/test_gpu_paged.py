@@ -796,3 +796,34 @@ def test_plan_on_either_side_of_one_block(cuda, capacity):
     table, ring, state, _ = pool_state(rng, ctx, 16, capacity // 16 + 20, 300)
     assert check_plan(ctx, new, table, ring, state, 16, capacity, in_place=True)["status"] == "ok"
     check_plan(ctx, new, table, ring, [state[0], 3], 16, capacity, in_place=True)
+
+
+@pytest.mark.parametrize("dn,dv,B", [(128, 128, 33), (64, 192, 5), (200, 72, 130), (8, 8, 300),
+                                     (264, 264, 40)])
+def test_decode_head_widths_and_batches(cuda, dn, dv, B):
+    """Nope and value widths either side of 128, batches either side of a
+    round and of a block of the projections."""
+    cfg = bf16(3, qk_nope_head_dim=dn, v_head_dim=dv, softmax_scale=0.07)
+    rng = np.random.default_rng(B)
+    check_decode(cfg, [int(x) for x in rng.integers(0, 300, B)], 16, seed=dn + dv)
+
+
+def test_decode_zero_and_huge_queries(cuda):
+    cfg = bf16(20)
+    d = decode_inputs(cfg, [300, 200, 100], 32, 15)
+    d["q_nope"][0] = 0
+    d["q_pe"][0] = 0
+    d["q_nope"][1] *= 2.0 ** 40
+    d["q_pe"][1] *= 2.0 ** 40
+    d["q_nope"][2, 3, 5] = float("inf")
+    out, _ = run_decode_paged(cfg, d, 32)
+    want = want_decode(cfg, d, 32)
+    assert torch.isnan(out[2].view(20, 128)[3].float()).all()
+    keep = [0, 2]
+    w = np.nan_to_num(want.reshape(3, 20, 128)[keep])
+    o = torch.nan_to_num(out.view(3, 20, 128)[keep].float())
+    w[1, 3] = 0
+    o[1, 3] = 0
+    assert oracle.max_rel_err(o, w) <= TOL["bf16"]
+    # at 2^40 one token takes all of the weight: a row of the cache, through W_UV
+    assert torch.isfinite(out[1].float()).all()
