@@ -286,12 +286,14 @@ def mla_decode_absorbed_noalloc(cfg, q_nope, q_pe, w_kv_b, latent_cache, cu_ctx,
 # their checks are one pass over the tensors: _ptr is asked for the words only
 # when something is wrong.
 def _torch():
-    global _T, _I32, _F32, _FP8, _U8, _DTYPES, _raw_stream
+    global _T, _I32, _F32, _FP8, _U8, _DTYPES, _raw_stream, _current_device
     import torch
     _T, _I32, _F32 = torch, torch.int32, torch.float32
     _FP8, _U8 = torch.float8_e4m3fn, torch.uint8
     _DTYPES = {MLA_BF16: torch.bfloat16, MLA_F32: torch.float32}
+    # without torch.cuda's bookkeeping around them, where torch has them
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     return torch
 
 
@@ -302,7 +304,7 @@ def _ptrs(workspace, tensors):
     """Device pointers of ``tensors``, (tensor, name, dtype, elements, optional)
     each, after the checks of ``_ptr``, and that all lie on the workspace's
     device, which has to be the current one (the kernels launch there)."""
-    dev = workspace.device if workspace is not None else None
+    dev = workspace.get_device() if workspace is not None else -1   # -1: not a GPU's
     out = []
     for t, name, dtype, numel, optional in tensors:
         if t is None:
@@ -310,20 +312,20 @@ def _ptrs(workspace, tensors):
                 raise ValueError(f"{name} is required")
             out.append(None)
             continue
-        if (t.dtype is not dtype or t.numel() < numel or not t.is_cuda
+        if (t.dtype is not dtype or t.numel() < numel or t.get_device() != dev or dev < 0
                 or not t.is_contiguous()):
             _ptr(t, name, optional, dtype, numel)
-        if t.device != dev and dev is not None:
-            raise ValueError(f"tensors on different devices: {name} on {t.device}, workspace "
-                             f"on {dev}")
+            if workspace is not None and t.device != workspace.device:
+                raise ValueError(f"tensors on different devices: {name} on {t.device}, workspace "
+                                 f"on {workspace.device}")
         out.append(t.data_ptr())
-    if workspace is None or not workspace.is_cuda or not workspace.is_contiguous():
+    if dev < 0 or not workspace.is_contiguous():
         _ptr(workspace, "workspace")
-    if dev.type == "cuda" and dev.index != _T.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, but the current device is "
-                         f"cuda:{_T.cuda.current_device()}")
+    elif dev != _current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is "
+                         f"cuda:{_current_device()}")
     out.append(workspace.data_ptr())
-    out.append(workspace.numel() * workspace.element_size())
+    out.append(workspace.nbytes)
     return out
 
 
@@ -331,7 +333,7 @@ def _stream_of(stream, workspace):
     if stream is None:
         if _raw_stream is None:
             return _T.cuda.current_stream().cuda_stream
-        return _raw_stream(workspace.device.index)
+        return _raw_stream(workspace.get_device())
     return getattr(stream, "cuda_stream", stream)
 
 

@@ -603,11 +603,20 @@ mla_status mla_decode_absorbed(const mla_config* cfg, const void* q_nope, const 
 
 mla_status mla_check_device_status(void* workspace, void* stream) {
   if (!workspace) return fail(MLA_ERR_NULL, "workspace is NULL");
-  uint32_t word = 0;
+  uint32_t head[2] = {0, 0}, words[mla::kMaxStatusSlots];
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = cudaMemcpyAsync(&word, workspace, 4, cudaMemcpyDeviceToHost, st);
+  cudaError_t e = cudaMemcpyAsync(head, workspace, 8, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, 4, st);
+  uint32_t word = head[0];
+  const uint32_t n = head[1] - mla::kStatusMagic;
+  if (e == cudaSuccess && head[1] >= mla::kStatusMagic && n <= (uint32_t)mla::kMaxStatusSlots) {
+    e = cudaMemcpyAsync(words, static_cast<uint32_t*>(workspace) + mla::kStatusSlots, 4 * n,
+                        cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess)
+      for (uint32_t i = 0; i < n; ++i) word |= words[i];
+  }
+  if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, 8, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(e, "status read");
   if (word & mla::kStatusTimeout) return fail(MLA_ERR_DEVICE_TIMEOUT, "status word 0x%x", word);

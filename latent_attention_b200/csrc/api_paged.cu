@@ -170,12 +170,14 @@ mla_status mla_paged_append(const mla_config* cfg, const void* rows, const int32
     return fail(MLA_ERR_ALIGN, "rows or cache is not 16-byte aligned");
   if (!aligned4(slot_map) || !aligned4(scales))
     return fail(MLA_ERR_ALIGN, "slot_map or scales is not 4-byte aligned");
-  const size_t need = 256 + 4 * (((size_t)n_blocks + 31) / 32);
+  const size_t bits = 4 * (((size_t)n_blocks + 31) / 32);
+  const size_t need = 256 + std::max<size_t>(4 * mla::kMaxStatusSlots, bits);
   s = check_workspace(workspace, workspace_bytes, need);
   if (s != MLA_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
   // the status word and the bit per block that claims it for one run
-  cudaError_t e = cudaMemsetAsync(workspace, 0, need, st);
+  if (n_rows > mla::kAppendScan) e = cudaMemsetAsync(workspace, 0, 256 + bits, st);
   if (e != cudaSuccess) return cuda_fail(e, "memset");
   uint32_t* ws = static_cast<uint32_t*>(workspace);
   e = mla::launch_paged_append(cfg->dtype, rows, slot_map, n_rows,
@@ -203,12 +205,10 @@ mla_status mla_paged_gather(const mla_config* cfg, const void* cache, const floa
     return fail(MLA_ERR_ALIGN, "cache or rows_out is not 16-byte aligned");
   if (!aligned4(scales) || !aligned4(block_table) || !aligned4(ctx_len) || !aligned4(cu_ctx))
     return fail(MLA_ERR_ALIGN, "scales, block_table, ctx_len or cu_ctx is not 4-byte aligned");
-  s = check_workspace(workspace, workspace_bytes, 256);
+  s = check_workspace(workspace, workspace_bytes, 256 + 4 * mla::kMaxStatusSlots);
   if (s != MLA_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = cudaMemsetAsync(workspace, 0, 256, st);
-  if (e != cudaSuccess) return cuda_fail(e, "memset");
-  e = mla::launch_paged_gather(cfg->dtype, pool_of(*cfg, cache, scales, n_blocks, block_size),
+  cudaError_t e = mla::launch_paged_gather(cfg->dtype, pool_of(*cfg, cache, scales, n_blocks, block_size),
                                block_table, ctx_len, rows_out, cu_ctx, B, max_blocks, capacity,
                                static_cast<uint32_t*>(workspace), st);
   if (e != cudaSuccess) return cuda_fail(e, "paged gather");

@@ -19,6 +19,13 @@ enum : uint32_t {
   kStatusNoBlocks = 1u << 3,  // paged cache: the plan needs more blocks or slots than there are
 };
 
+// The status word stands first in a workspace.  A call that would need a launch
+// of its own just to clear it leaves a word per block instead, from
+// kStatusSlots (32-bit words) on, and says so in the second word: their OR is the
+// status.  Every other call leaves 0 there.
+constexpr uint32_t kStatusMagic = 0x5a750000u;      // | number of words
+constexpr int kStatusSlots = 64, kMaxStatusSlots = 2048;
+
 template <typename T> struct Elem;
 template <> struct Elem<float> {
   static __device__ __forceinline__ float load(const float* p) { return *p; }
@@ -246,6 +253,10 @@ cudaError_t launch_latent_finalize(int dtype, const void* ckv,
                                    cudaStream_t st, int T = 1, int dst_T = 1, int dst_off = 0);
 cudaError_t launch_decode_simt(int dtype, const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st);
+// Rows up to which an append finds a block's second run by looking through the
+// slots before it; beyond, a bit per block (claims, zeroed with the status)
+// tells.
+constexpr int kAppendScan = 4096;
 cudaError_t launch_paged_append(int dtype, const void* rows, const int32_t* slots, int n_rows,
                                 const PagedPool& pool, uint32_t* status, uint32_t* claims,
                                 cudaStream_t st);

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int alon
   if (t == 0) {
     s_head = a.state[0];
     s_count = a.state[1];
-    *a.status = 0;
+    a.status[0] = a.status[1] = 0;
   }
   const int per = (a.B + kPlanThreads - 1) / kPlanThreads, b0 = t * per, b1 = min(b0 + per, a.B);
   int64_t add = 0, give = 0, fresh = 0;
@@ -197,6 +197,22 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(PlanArgs a) {
 // kHeld pieces of 16 a thread, 32 rows of 576; longer runs are read again),
 // so that memory sees them once.
 constexpr int kAppendThreads = 256;
+
+// A block's status at its end (of all threads, after a barrier): a word of its
+// own, or into the status word that was cleared before the launch.
+__device__ __forceinline__ void report(uint32_t* status, uint32_t flags, bool own) {
+  if (threadIdx.x != 0) return;
+  if (own) {
+    status[kStatusSlots + blockIdx.x] = flags;
+    if (blockIdx.x == 0) {
+      status[0] = 0;
+      status[1] = kStatusMagic + gridDim.x;
+    }
+  } else if (flags) {
+    atomicOr(status, flags);
+  }
+}
+
 constexpr int kHeld = 5;
 
 template <typename T>
@@ -207,11 +223,15 @@ __global__ void __launch_bounds__(kAppendThreads)
   __shared__ int starts[128], n_starts;
   __shared__ int s_len, s_ok;               // run length; the block is this run's
   __shared__ uint32_t s_amax, s_odd;        // largest finite |value|, any NaN or infinity
+  __shared__ uint32_t flags;                // this block's status
   const int t = threadIdx.x, W = pool.W, bs = pool.bs;
   const int64_t n_slots = (int64_t)pool.n_blocks * bs;
   const bool wide = aligned32(rows);        // rows are a multiple of 32 bytes
   const int w0 = blockIdx.x * window, w1 = min(w0 + window, n_rows);
-  if (t == 0) n_starts = 0;
+  if (t == 0) {
+    n_starts = 0;
+    flags = 0;
+  }
   for (int k = t; k < w1 - w0 + bs + 1; k += kAppendThreads) {
     const int i = w0 - 1 + k;
     sl[k] = i >= 0 && i < n_rows ? slots[i] : -1;
@@ -223,7 +243,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     // a row of the block that the row before it writes: part of that run, or
     // (not its next slot) refused
     const bool cont = in && before >= 0 && before / bs == s / bs;
-    if ((!in && s != -1) || (cont && before + 1 != s)) atomicOr(status, kStatusBadPage);
+    if ((!in && s != -1) || (cont && before + 1 != s)) atomicOr(&flags, kStatusBadPage);
     if (in && !cont) starts[atomicAdd(&n_starts, 1)] = w0 + t;
   }
   __syncthreads();
@@ -235,6 +255,7 @@ __global__ void __launch_bounds__(kAppendThreads)
       s_len = most;
       s_amax = 0;
       s_odd = 0;
+      s_ok = 1;
     }
     __syncthreads();
     if (t < most && sl[i - w0 + 1 + t] != s + t) atomicMin(&s_len, t);
@@ -245,11 +266,14 @@ __global__ void __launch_bounds__(kAppendThreads)
 #pragma unroll
     for (int q = 0; q < kHeld; ++q)
       if (t + q * kAppendThreads < nv) load_piece(src + (t + q * kAppendThreads) * 16, wide, held[q]);
-    if (t == 0) {
-      // two runs of one call in one block have no order: the second is refused
+    // two runs of one call in one block have no order: the second is refused
+    if (claims) {
       const uint32_t bit = 1u << (blk & 31);
-      s_ok = !(atomicOr(&claims[blk >> 5], bit) & bit);
-      if (!s_ok) atomicOr(status, kStatusBadPage);
+      if (t == 0 && (atomicOr(&claims[blk >> 5], bit) & bit)) s_ok = 0;
+    } else {
+      bool taken = false;
+      for (int q = t; q < i; q += kAppendThreads) taken |= slots[q] >= 0 && slots[q] / bs == blk;
+      if (taken) s_ok = 0;
     }
     const float old_scale = off > 0 ? pool.scales[blk] : 1.f;
     uint32_t amax = 0, odd = 0;
@@ -284,7 +308,7 @@ __global__ void __launch_bounds__(kAppendThreads)
         if (stored_exp(old_scale, &e_old)) {
           e = max(e, e_old);
         } else {
-          if (t == 0) atomicOr(status, kStatusBadPage);
+          if (t == 0) flags |= kStatusBadPage;
           e_old = e;
         }
       }
@@ -324,9 +348,12 @@ __global__ void __launch_bounds__(kAppendThreads)
         put(p, x);
       }
       if (t == 0) pool.scales[blk] = pow2(e);
+    } else if (t == 0) {
+      flags |= kStatusBadPage;
     }
     __syncthreads();                         // this run's shared values are read
   }
+  report(status, flags, !claims);
 }
 
 // ----------------------------------------------------------------- gather
@@ -346,7 +373,9 @@ __global__ void __launch_bounds__(kGatherThreads)
   __shared__ int64_t warp_sum[kGatherThreads / 32];
   __shared__ int64_t src[2][kGatherRows];    // byte offset of a tile's rows, or -1
   __shared__ float scl[2][kGatherRows];
+  __shared__ uint32_t flags;                 // this block's status
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (t == 0) flags = 0;
   const int64_t most = (int64_t)max_blocks * pool.bs;
   const int per = (B + kGatherThreads - 1) / kGatherThreads;
   const int b0 = min(t * per, B), b1 = min(b0 + per, B);
@@ -372,7 +401,7 @@ __global__ void __launch_bounds__(kGatherThreads)
   __syncthreads();
   const int total = ends[B - 1];
   if (blockIdx.x == 0) {
-    if (bad || (t == 0 && total > capacity)) atomicOr(status, kStatusBadPage);
+    if (bad || (t == 0 && total > capacity)) atomicOr(&flags, kStatusBadPage);
     if (t == 0) cu[0] = 0;
   }
   const int n_rows = min(total, capacity), nv = pool.W / 16;
@@ -393,7 +422,7 @@ __global__ void __launch_bounds__(kGatherThreads)
           o = ((int64_t)blk * pool.bs + j % pool.bs) * pool.W;
           s = pool.scales[blk];
         } else {
-          atomicOr(status, kStatusBadPage);
+          atomicOr(&flags, kStatusBadPage);
         }
       }
       src[buf][t] = o;
@@ -432,6 +461,8 @@ __global__ void __launch_bounds__(kGatherThreads)
       }
     }
   }
+  __syncthreads();
+  report(status, flags, true);
 }
 
 }  // namespace
@@ -456,6 +487,7 @@ cudaError_t launch_paged_append(int dtype, const void* rows, const int32_t* slot
   int window = (n_rows + 4 * 148 - 1) / (4 * 148);
   if (window > pool.bs) window = pool.bs;
   const int grid = (n_rows + window - 1) / window;
+  if (n_rows <= kAppendScan) claims = nullptr;   // (at most 592 blocks)
   count_launches();
   if (dtype == MLA_F32)
     append_kernel<float><<<grid, kAppendThreads, 0, st>>>((const float*)rows, slots, n_rows, pool,

@@ -16,7 +16,8 @@ template <typename T>
 __global__ void paged_absorb_kernel(PagedDecodeArgs a) {
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+    a.status[0] = a.status[1] = 0;
   const int b = blockIdx.x, hh = blockIdx.y;
   extern __shared__ float qn[];
   const T* qnope = reinterpret_cast<const T*>(a.q_nope) + ((int64_t)b * a.h + hh) * a.dn;

@@ -109,7 +109,7 @@ __device__ __forceinline__ uint32_t finite_bits(float& x) {
 __device__ void lengths(const QueryParams& p) {
   __shared__ int64_t sums[NT / 32];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (t == 0) *p.status = 0;
+  if (t == 0) p.status[0] = p.status[1] = 0;
   __syncthreads();
   const int per = (p.B + NT - 1) / NT, b0 = min(t * per, p.B), b1 = min(b0 + per, p.B);
   int64_t sum = 0;

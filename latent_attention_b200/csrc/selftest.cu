@@ -24,7 +24,7 @@ extern "C" mla_status mla_selftest_wait_timeout(void* workspace, void* stream) {
   if (!workspace) return MLA_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MLA_ERR_ALIGN;
   cudaStream_t st = (cudaStream_t)stream;
-  if (cudaMemsetAsync(workspace, 0, 4, st) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaMemsetAsync(workspace, 0, 8, st) != cudaSuccess) return MLA_ERR_CUDA;
   mla::wait_timeout_kernel<<<1, 32, 0, st>>>(static_cast<uint32_t*>(workspace));
   mla::count_launches();
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
