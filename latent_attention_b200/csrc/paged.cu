@@ -192,11 +192,13 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(PlanArgs a) {
 // block; one CTA quantises it:  e = min{e : max|row| <= 448 2^e}; rows of the
 // block in front of the run (offsets below its first slot) are kept and moved
 // to max(e, e_old).  Rows behind the run are dead and stay as they were.
-// A CTA takes the runs that start in its window of the slot map, and holds a
-// run's values in registers between the maximum and the rounding (the first
-// kHeld pieces of 16 a thread, 32 rows of 576; longer runs are read again),
-// so that memory sees them once.
-constexpr int kAppendThreads = 256;
+// A CTA takes the runs that start in its window of the slot map.  A run's values
+// stay in registers between the maximum and the rounding (the first HELD pieces
+// of 16 a thread; the rest of a longer run is read again).  Where a window of
+// a 1024-thread block holds more than two runs, those of up to kShortRun rows
+// take a warp each and go side by side (the new tokens of many requests); the
+// others take the whole block.  (256-thread blocks do without: the mere code
+// cost 48624 rows in 1500 runs 4 us of 23.)
 
 // A block's status at its end (of all threads, after a barrier): a word of its
 // own, or into the status word that was cleared before the launch.
@@ -213,18 +215,112 @@ __device__ __forceinline__ void report(uint32_t* status, uint32_t flags, bool ow
   }
 }
 
-constexpr int kHeld = 5;
+constexpr int kShortRun = 4;
 
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads)
+__device__ __forceinline__ void maxima(const Piece<T>& x, uint32_t& amax, uint32_t& odd) {
+  float v[16];
+  values(x, v);
+#pragma unroll
+  for (int y = 0; y < 16; ++y) {
+    const uint32_t b = __float_as_uint(v[y]) & 0x7fffffffu;
+    if (b < 0x7f800000u) amax = max(amax, b); else odd = 1;
+  }
+}
+__device__ __forceinline__ uint4 to_bytes(const float (&v)[16]) {
+  return make_uint4(to_e4m3x4(v[0], v[1], v[2], v[3]), to_e4m3x4(v[4], v[5], v[6], v[7]),
+                    to_e4m3x4(v[8], v[9], v[10], v[11]), to_e4m3x4(v[12], v[13], v[14], v[15]));
+}
+
+// One run by G threads (a warp or the block).  share(amax, odd, refused) makes
+// the three values those of all threads; odd: any NaN or infinity.
+template <typename T, int G, int HELD, typename Share>
+__device__ __forceinline__ void append_run(const T* __restrict__ rows,
+                                           const int32_t* __restrict__ slots, const PagedPool& pool,
+                                           int i, int s, int len, int t, bool wide,
+                                           uint32_t* claims, uint32_t* flags, Share share) {
+  const int W = pool.W, bs = pool.bs, blk = s / bs, off = s % bs, nv = len * W / 16;
+  const T* src = rows + (int64_t)i * W;
+  Piece<T> held[HELD];
+#pragma unroll
+  for (int q = 0; q < HELD; ++q)
+    if (t + q * G < nv) load_piece(src + (t + q * G) * 16, wide, held[q]);
+  // two runs of one call in one block have no order: the second is refused
+  uint32_t refused = 0;
+  if (claims) {
+    const uint32_t bit = 1u << (blk & 31);
+    if (t == 0 && (atomicOr(&claims[blk >> 5], bit) & bit)) refused = 1;
+  } else {
+    for (int q = t; q < i; q += G) refused |= slots[q] >= 0 && slots[q] / bs == blk;
+  }
+  const float old_scale = off > 0 ? pool.scales[blk] : 1.f;
+  uint32_t amax = 0, odd = 0;
+#pragma unroll
+  for (int q = 0; q < HELD; ++q)
+    if (t + q * G < nv) maxima(held[q], amax, odd);
+  for (int p = t + HELD * G; p < nv; p += G) {
+    Piece<T> x;
+    load_piece(src + p * 16, wide, x);
+    maxima(x, amax, odd);
+  }
+  share(amax, odd, refused);
+  if (refused) {
+    if (t == 0) atomicOr(flags, kStatusBadPage);
+    return;
+  }
+  int e = scale_exp(amax), e_old = e;
+  uint8_t* base = pool.cache + (int64_t)blk * bs * W;
+  if (off > 0) {
+    if (stored_exp(old_scale, &e_old)) {
+      e = max(e, e_old);
+    } else {
+      if (t == 0) atomicOr(flags, kStatusBadPage);
+      e_old = e;
+    }
+  }
+  if (e != e_old) {                          // the kept rows move to the larger scale
+    const float f = pow2(e_old - e);
+    uint4* kept = reinterpret_cast<uint4*>(base);
+#pragma unroll 4
+    for (int p = t; p < off * W / 16; p += G) {
+      float v[16];
+      dequant16(kept[p], f, v);
+      kept[p] = to_bytes(v);
+    }
+  }
+  const float f = pow2(-e);
+  uint4* dst = reinterpret_cast<uint4*>(base + (int64_t)off * W);
+  auto put = [&](int p, const Piece<T>& x) {
+    float v[16];
+    values(x, v);
+#pragma unroll
+    for (int y = 0; y < 16; ++y) {
+      // an infinity is stored as NaN, not as 448: x - x is NaN for both
+      if (odd) v[y] += v[y] - v[y];
+      v[y] *= f;
+    }
+    dst[p] = to_bytes(v);
+  };
+#pragma unroll
+  for (int q = 0; q < HELD; ++q)
+    if (t + q * G < nv) put(t + q * G, held[q]);
+  for (int p = t + HELD * G; p < nv; p += G) {
+    Piece<T> x;
+    load_piece(src + p * 16, wide, x);
+    put(p, x);
+  }
+  if (t == 0) pool.scales[blk] = pow2(e);    // (every thread has read it: share)
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT)
     append_kernel(const T* __restrict__ rows, const int32_t* __restrict__ slots, int n_rows,
                   PagedPool pool, int window, uint32_t* status, uint32_t* claims) {
+  constexpr int HELD = NT == 256 ? 5 : sizeof(T) == 2 ? 3 : 2;
   __shared__ int sl[258];                   // slots w0 - 1 .. w1 + bs - 1
-  __shared__ int starts[128], n_starts;
-  __shared__ int s_len, s_ok;               // run length; the block is this run's
-  __shared__ uint32_t s_amax, s_odd;        // largest finite |value|, any NaN or infinity
-  __shared__ uint32_t flags;                // this block's status
-  const int t = threadIdx.x, W = pool.W, bs = pool.bs;
+  __shared__ int starts[128], lens[128], n_starts, run_len;
+  __shared__ uint32_t s_val[3], flags;      // a run's maximum, odd, refused; this block's status
+  const int t = threadIdx.x, bs = pool.bs;
   const int64_t n_slots = (int64_t)pool.n_blocks * bs;
   const bool wide = aligned32(rows);        // rows are a multiple of 32 bytes
   const int w0 = blockIdx.x * window, w1 = min(w0 + window, n_rows);
@@ -232,7 +328,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     n_starts = 0;
     flags = 0;
   }
-  for (int k = t; k < w1 - w0 + bs + 1; k += kAppendThreads) {
+  for (int k = t; k < w1 - w0 + bs + 1; k += NT) {
     const int i = w0 - 1 + k;
     sl[k] = i >= 0 && i < n_rows ? slots[i] : -1;
   }
@@ -244,115 +340,57 @@ __global__ void __launch_bounds__(kAppendThreads)
     // (not its next slot) refused
     const bool cont = in && before >= 0 && before / bs == s / bs;
     if ((!in && s != -1) || (cont && before + 1 != s)) atomicOr(&flags, kStatusBadPage);
-    if (in && !cont) starts[atomicAdd(&n_starts, 1)] = w0 + t;
+    if (in && !cont) {
+      const int k = atomicAdd(&n_starts, 1), most = min(bs - s % bs, n_rows - w0 - t);
+      int len = 1;                          // up to kShortRun + 1
+      while (len <= kShortRun && len < most && sl[t + 1 + len] == s + len) ++len;
+      starts[k] = w0 + t;
+      lens[k] = len;
+    }
   }
   __syncthreads();
   const int todo = n_starts;
-  for (int k = 0; k < todo; ++k) {
-    const int i = starts[k], s = sl[i - w0 + 1], blk = s / bs, off = s % bs;
-    const int most = min(bs - off, n_rows - i);
-    if (t == 0) {
-      s_len = most;
-      s_amax = 0;
-      s_odd = 0;
-      s_ok = 1;
-    }
-    __syncthreads();
-    if (t < most && sl[i - w0 + 1 + t] != s + t) atomicMin(&s_len, t);
-    __syncthreads();
-    const T* src = rows + (int64_t)i * W;
-    const int nv = s_len * W / 16;
-    Piece<T> held[kHeld];
-#pragma unroll
-    for (int q = 0; q < kHeld; ++q)
-      if (t + q * kAppendThreads < nv) load_piece(src + (t + q * kAppendThreads) * 16, wide, held[q]);
-    // two runs of one call in one block have no order: the second is refused
-    if (claims) {
-      const uint32_t bit = 1u << (blk & 31);
-      if (t == 0 && (atomicOr(&claims[blk >> 5], bit) & bit)) s_ok = 0;
-    } else {
-      bool taken = false;
-      for (int q = t; q < i; q += kAppendThreads) taken |= slots[q] >= 0 && slots[q] / bs == blk;
-      if (taken) s_ok = 0;
-    }
-    const float old_scale = off > 0 ? pool.scales[blk] : 1.f;
-    uint32_t amax = 0, odd = 0;
-    auto look = [&](const Piece<T>& x) {
-      float v[16];
-      values(x, v);
-#pragma unroll
-      for (int y = 0; y < 16; ++y) {
-        const uint32_t b = __float_as_uint(v[y]) & 0x7fffffffu;
-        if (b < 0x7f800000u) amax = max(amax, b); else odd = 1;
-      }
-    };
-#pragma unroll
-    for (int q = 0; q < kHeld; ++q)
-      if (t + q * kAppendThreads < nv) look(held[q]);
-    for (int p = t + kHeld * kAppendThreads; p < nv; p += kAppendThreads) {
-      Piece<T> x;
-      load_piece(src + p * 16, wide, x);
-      look(x);
-    }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    odd = __reduce_or_sync(0xffffffffu, odd);
-    if ((t & 31) == 0) {
-      atomicMax(&s_amax, amax);
-      if (odd) atomicOr(&s_odd, 1u);
-    }
-    __syncthreads();
-    if (s_ok) {
-      int e = scale_exp(s_amax), e_old = e;
-      uint8_t* base = pool.cache + (int64_t)blk * bs * W;
-      if (off > 0) {
-        if (stored_exp(old_scale, &e_old)) {
-          e = max(e, e_old);
-        } else {
-          if (t == 0) flags |= kStatusBadPage;
-          e_old = e;
-        }
-      }
-      if (e != e_old) {                      // the kept rows move to the larger scale
-        const float f = pow2(e_old - e);
-        uint4* kept = reinterpret_cast<uint4*>(base);
-        for (int p = t; p < off * W / 16; p += kAppendThreads) {
-          float v[16];
-          dequant16(kept[p], f, v);
-          kept[p] = make_uint4(to_e4m3x4(v[0], v[1], v[2], v[3]), to_e4m3x4(v[4], v[5], v[6], v[7]),
-                               to_e4m3x4(v[8], v[9], v[10], v[11]),
-                               to_e4m3x4(v[12], v[13], v[14], v[15]));
-        }
-      }
-      const float f = pow2(-e);
-      uint4* dst = reinterpret_cast<uint4*>(base + (int64_t)off * W);
-      const bool any_odd = s_odd != 0;
-      auto put = [&](int p, const Piece<T>& x) {
-        float v[16];
-        values(x, v);
-#pragma unroll
-        for (int y = 0; y < 16; ++y) {
-          // an infinity is stored as NaN, not as 448: x - x is NaN for both
-          if (any_odd) v[y] += v[y] - v[y];
-          v[y] *= f;
-        }
-        dst[p] = make_uint4(to_e4m3x4(v[0], v[1], v[2], v[3]), to_e4m3x4(v[4], v[5], v[6], v[7]),
-                            to_e4m3x4(v[8], v[9], v[10], v[11]),
-                            to_e4m3x4(v[12], v[13], v[14], v[15]));
-      };
-#pragma unroll
-      for (int q = 0; q < kHeld; ++q)
-        if (t + q * kAppendThreads < nv) put(t + q * kAppendThreads, held[q]);
-      for (int p = t + kHeld * kAppendThreads; p < nv; p += kAppendThreads) {
-        Piece<T> x;
-        load_piece(src + p * 16, wide, x);
-        put(p, x);
-      }
-      if (t == 0) pool.scales[blk] = pow2(e);
-    } else if (t == 0) {
-      flags |= kStatusBadPage;
-    }
-    __syncthreads();                         // this run's shared values are read
+  const bool apart = NT == 1024 && todo > 2;
+  if constexpr (NT == 1024) {
+    for (int k = t / 32; apart && k < todo; k += NT / 32)
+      if (lens[k] <= kShortRun)
+        append_run<T, 32, sizeof(T) == 2 ? 5 : 2>(rows, slots, pool, starts[k], sl[starts[k] - w0 + 1], lens[k], t & 31,
+                             wide, claims, &flags,
+                             [](uint32_t& amax, uint32_t& odd, uint32_t& refused) {
+                               amax = __reduce_max_sync(0xffffffffu, amax);
+                               odd = __reduce_or_sync(0xffffffffu, odd);
+                               refused = __reduce_or_sync(0xffffffffu, refused);
+                             });
   }
+  for (int k = 0; k < todo; ++k) {
+    if (apart && lens[k] <= kShortRun) continue;
+    const int i = starts[k], s = sl[i - w0 + 1];
+    const int most = min(bs - s % bs, n_rows - i);
+    __syncthreads();                        // the run before is done with the shared values
+    if (t == 0) {
+      run_len = most;
+      s_val[0] = s_val[1] = s_val[2] = 0;
+    }
+    __syncthreads();
+    if (t < most && sl[i - w0 + 1 + t] != s + t) atomicMin(&run_len, t);
+    __syncthreads();
+    append_run<T, NT, HELD>(rows, slots, pool, i, s, run_len, t, wide, claims, &flags,
+                            [&](uint32_t& amax, uint32_t& odd, uint32_t& refused) {
+                              amax = __reduce_max_sync(0xffffffffu, amax);
+                              odd = __reduce_or_sync(0xffffffffu, odd);
+                              refused = __reduce_or_sync(0xffffffffu, refused);
+                              if ((t & 31) == 0) {
+                                atomicMax(&s_val[0], amax);
+                                if (odd) atomicOr(&s_val[1], 1u);
+                                if (refused) atomicOr(&s_val[2], 1u);
+                              }
+                              __syncthreads();
+                              amax = s_val[0];
+                              odd = s_val[1];
+                              refused = s_val[2];
+                            });
+  }
+  __syncthreads();
   report(status, flags, !claims);
 }
 
@@ -484,17 +522,27 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
 cudaError_t launch_paged_append(int dtype, const void* rows, const int32_t* slots, int n_rows,
                                 const PagedPool& pool, uint32_t* status, uint32_t* claims,
                                 cudaStream_t st) {
-  int window = (n_rows + 4 * 148 - 1) / (4 * 148);
-  if (window > pool.bs) window = pool.bs;
+  // Fewer runs of whole blocks than twice the SMs: blocks of 1024 threads, one an
+  // SM (4096 rows in 64 runs 6.2 us, against 10.2 with four windows an SM, whose
+  // empty blocks are in the way, and 11.0 with 256 threads).  Beyond: 256 threads
+  // and four windows an SM, whose blocks overlap each other's trips to memory.
+  const bool few = n_rows < 2 * 148 * pool.bs;
+  const int windows = few ? 148 : 4 * 148;
+  const int window = std::min((n_rows + windows - 1) / windows, pool.bs);
   const int grid = (n_rows + window - 1) / window;
   if (n_rows <= kAppendScan) claims = nullptr;   // (at most 592 blocks)
   count_launches();
-  if (dtype == MLA_F32)
-    append_kernel<float><<<grid, kAppendThreads, 0, st>>>((const float*)rows, slots, n_rows, pool,
-                                                          window, status, claims);
-  else
-    append_kernel<__nv_bfloat16><<<grid, kAppendThreads, 0, st>>>(
-        (const __nv_bfloat16*)rows, slots, n_rows, pool, window, status, claims);
+  const auto go = [&](auto kernel, auto* p, int nt) {
+    kernel<<<grid, nt, 0, st>>>(p, slots, n_rows, pool, window, status, claims);
+  };
+  if (dtype == MLA_F32) {
+    if (few) go(append_kernel<float, 1024>, (const float*)rows, 1024);
+    else go(append_kernel<float, 256>, (const float*)rows, 256);
+  } else {
+    const auto* p = (const __nv_bfloat16*)rows;
+    if (few) go(append_kernel<__nv_bfloat16, 1024>, p, 1024);
+    else go(append_kernel<__nv_bfloat16, 256>, p, 256);
+  }
   return cudaGetLastError();
 }
 

@@ -827,3 +827,39 @@ def test_decode_zero_and_huge_queries(cuda):
     assert oracle.max_rel_err(o, w) <= TOL["bf16"]
     # at 2^40 one token takes all of the weight: a row of the cache, through W_UV
     assert torch.isfinite(out[1].float()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n_runs,rows_max", [(700, 1), (1500, 5), (4500, 1), (300, 9)])
+def test_append_of_many_short_runs(cuda, dtype, n_runs, rows_max):
+    """The new tokens of many requests: runs of a few rows, several a window,
+    with and without kept rows, some windows with a long one among them."""
+    cfg = bf16(2) if dtype == "bf16" else F32
+    rng = np.random.default_rng(n_runs)
+    bs = 16
+    runs = [(int(rng.integers(0, bs - rows_max + 1)), int(rng.integers(1, rows_max + 1)))
+            for _ in range(n_runs)]
+    runs[5] = (0, bs)
+    slots = slots_for(rng, n_runs + 3, bs, runs)
+    slots[-1] = -1
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    check_append(cfg, random_rows(len(slots), width(cfg), dt, n_runs), slots,
+                 *dirty_pool(n_runs + 3, bs, width(cfg), 11), bs)
+
+
+def test_append_refuses_a_second_run_among_many(cuda):
+    """Below and above the count from which blocks are claimed by a bit."""
+    for n in (300, 4600):
+        slots = [16 * i for i in range(n)]
+        slots[n - 2] = 16 * 7 + 3
+        cache, scales = dirty_pool(n, 16, width(F32), 12)
+        rows = random_rows(n, width(F32), torch.float32, 13)
+        got, sc, ws = run_append(F32, rows, slots, cache, scales, 16)
+        with pytest.raises(L.MlaError, match="SHAPE"):
+            L.mla_check_device_status(ws)
+        L.mla_check_device_status(ws)               # read once
+        ok = [i for i in range(n) if i not in (7, n - 2)]
+        want, wsc = O.append(rows[ok], [slots[i] for i in ok], cache.numpy(), scales.numpy(), 16)
+        idx = [slots[i] // 16 for i in ok]
+        assert np.array_equal(sc[idx], wsc[idx])
+        assert np.array_equal(O.E4M3[got[idx]], O.E4M3[want[idx]])
