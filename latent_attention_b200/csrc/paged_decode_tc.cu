@@ -140,14 +140,33 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       : "memory");
 }
 // The same with a ue8m0 scale per row and 32 values of K of either operand.
+// A may stay in the tensor core's collector for the next product with it
+// (KEEP: fill) or come from there (USE: last use), which saves reading it.
+enum Collector { NONE, KEEP, USE };
+template <Collector C>
 __device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t sfa, uint32_t sfb, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
-      "[%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-      : "memory");
+  if (C == KEEP)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X.collector::a::fill "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+  else if (C == USE)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X.collector::a::lastuse "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
 }
 // 32 rows of 16 bytes into 4 TMEM columns, repeated in all four lane quarters.
 __device__ __forceinline__ void tmem_cp_sf(uint32_t taddr, uint64_t desc) {
@@ -456,13 +475,18 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
         for (int a = 0; a < 4; ++a) {
           const uint64_t dc = dc0 + (uint64_t)((slot * BOX) >> 4);
 #pragma unroll
-          for (int term = 0; term < (K::STK ? 1 : 2); ++term)
-#pragma unroll
-            for (int kb = 0; kb < 4; ++kb)
-              mma_mxf8(tbase + K::TM_O + a * K::PN, dc + (uint64_t)((kb * 32 * 128) >> 4),
-                       dp + (uint64_t)((term * CT * 64 + kb * 32 * K::PW) >> 4),
-                       idesc_mxf8(K::PN, kb), tbase + K::TM_SFA, sfb,
-                       term || kb ? 1u : keep);
+          for (int kb = 0; kb < 4; ++kb) {
+            const uint32_t to = tbase + K::TM_O + a * K::PN, sfa = tbase + K::TM_SFA;
+            const uint64_t da = dc + (uint64_t)((kb * 32 * 128) >> 4);
+            const uint64_t db = dp + (uint64_t)((kb * 32 * K::PW) >> 4);
+            const uint32_t id = idesc_mxf8(K::PN, kb), acc = kb ? 1u : keep;
+            if (K::STK) {
+              mma_mxf8<NONE>(to, da, db, id, sfa, sfb, acc);
+            } else {
+              mma_mxf8<KEEP>(to, da, db, id, sfa, sfb, acc);
+              mma_mxf8<USE>(to, da, db + (uint64_t)((CT * 64) >> 4), id, sfa, sfb, 1);
+            }
+          }
           mma_commit(&sh.c_empty[slot]);
           if (++slot == NS) slot = 0;
         }
@@ -726,6 +750,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
         __syncwarp();
         const uint32_t pt = p_base + pb * K::PBYTES;
         constexpr uint32_t lo_at = K::STK ? NH : 0, lo_tile = K::STK ? 0 : CT * 64;
+        uint32_t hb[HPG / 4], lb[HPG / 4];
 #pragma unroll
         for (int i = 0; i < HPG; i += 8) {
           uint32_t hi[2], lo[2];
@@ -745,9 +770,16 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
             lo[q] = f16x2_to_e4m3x2(sub_f16x2(w01, e4m3x2_to_f16x2(h01))) |
                     (f16x2_to_e4m3x2(sub_f16x2(w23, e4m3x2_to_f16x2(h23))) << 16);
           }
-          const uint32_t at = row * K::PW + h0 + i;
-          st_shared_v2(pt + swz<K::PW>(at), hi[0], hi[1]);
-          st_shared_v2(pt + lo_tile + swz<K::PW>(at + lo_at), lo[0], lo[1]);
+          hb[i / 4] = hi[0]; hb[i / 4 + 1] = hi[1];
+          lb[i / 4] = lo[0]; lb[i / 4 + 1] = lo[1];
+        }
+        const uint32_t at = row * K::PW + h0;
+        if constexpr (HPG == 16) {
+          st_shared_v4(pt + swz<K::PW>(at), hb[0], hb[1], hb[2], hb[3]);
+          st_shared_v4(pt + lo_tile + swz<K::PW>(at + lo_at), lb[0], lb[1], lb[2], lb[3]);
+        } else {
+          st_shared_v2(pt + swz<K::PW>(at), hb[0], hb[1]);
+          st_shared_v2(pt + lo_tile + swz<K::PW>(at + lo_at), lb[0], lb[1]);
         }
         // a weight of 0 times whatever lies behind the last token could be NaN
         if (!live) {
