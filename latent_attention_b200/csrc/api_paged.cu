@@ -97,7 +97,8 @@ void paged_layout(const mla_config& c, int B, int max_blocks, int block_size,
   L->part_o = take(parts * h * r * 4);
   L->part_lse = take(parts * h * 4);
   L->o_lat = take(B * h * r * (mla::tc_paged_supported(c) ? 4 : es));
-  L->o = take(B * h * c.v_head_dim * es);
+  // on tensor cores o is two terms for the projection behind it
+  L->o = take(B * h * c.v_head_dim * es * (mla::tc_paged_supported(c) ? 2 : 1));
   L->total_bytes = off;
 }
 
@@ -106,7 +107,12 @@ mla_status check_decode(const mla_config& c, bool o_proj, int max_blocks, int bl
   mla_status s = check_row(c);
   if (s != MLA_OK) return s;
   const int w = c.kv_lora_rank + c.qk_rope_head_dim;
-  if (mla::tc_paged_supported(c)) return MLA_OK;
+  if (mla::tc_paged_supported(c)) {
+    if (o_proj && !mla::tc_paged_oproj_supported(c))
+      return fail(MLA_ERR_UNSUPPORTED, "paged decode: hidden_size=%d is not a multiple of 8",
+                  c.hidden_size);
+    return MLA_OK;
+  }
   if (std::max(mla::paged_simt_smem(w, kSimtSplit), 4 * (c.kv_lora_rank + 256)) > mla::kMaxSmem)
     return fail(MLA_ERR_UNSUPPORTED, "paged decode: kv_lora_rank + qk_rope_head_dim = %d is too large", w);
   if ((int64_t)max_blocks * block_size > 65535ll * kSimtSplit)
@@ -269,6 +275,7 @@ mla_status mla_decode_paged(const mla_config* cfg, const void* q_nope, const voi
   a.part_o = (float*)(ws + L.part_o); a.part_lse = (float*)(ws + L.part_lse);
   a.o_lat = ws + L.o_lat;
   a.o = w_o ? ws + L.o : out;
+  a.o_lo = w_o && tc ? ws + L.o + (int64_t)B * a.h * a.dv * 2 : nullptr;
   a.status = (uint32_t*)(ws + L.status);
   if (tc) {
     a.tc = mla::tc_paged_plan(a.h, L.max_splits / 2);
@@ -286,12 +293,16 @@ mla_status mla_decode_paged(const mla_config* cfg, const void* q_nope, const voi
   if (e != cudaSuccess) return cuda_fail(e, "paged decode");
   mla::stage_event(4, st);
   if (w_o) {
-    mla::GemmArgs go;
-    go.A = a.o; go.lda = (int64_t)a.h * a.dv; go.M = B; go.K = a.h * a.dv; go.nseg = 1;
-    go.Bm[0] = w_o; go.ldb[0] = (int64_t)a.h * a.dv;
-    go.seg[0].out = out; go.seg[0].ldo = c.hidden_size; go.seg[0].ncols = c.hidden_size;
-    e = mla::tc_gemm_supported(go, c.dtype) ? mla::tc_gemm(go, st, a.status)
-                                           : mla::launch_gemm_simt(c.dtype, go, st);
+    if (tc) {
+      e = mla::launch_paged_oproj(a.o, a.o_lo, w_o, out, B, a.h * a.dv, c.hidden_size, a.status, st);
+    } else {
+      mla::GemmArgs go;
+      go.A = a.o; go.lda = (int64_t)a.h * a.dv; go.M = B; go.K = a.h * a.dv; go.nseg = 1;
+      go.Bm[0] = w_o; go.ldb[0] = (int64_t)a.h * a.dv;
+      go.seg[0].out = out; go.seg[0].ldo = c.hidden_size; go.seg[0].ncols = c.hidden_size;
+      e = mla::tc_gemm_supported(go, c.dtype) ? mla::tc_gemm(go, st, a.status)
+                                             : mla::launch_gemm_simt(c.dtype, go, st);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "paged decode o_proj");
   }
   mla::stage_event(5, st);

@@ -170,6 +170,7 @@ struct PagedDecodeArgs {
   float *part_o, *part_lse;        // [B, max_splits, h, r], [B, max_splits, h]
   void* o_lat;                     // [B, h, r]
   void* o;                         // [B, h, dv]
+  void* o_lo;                      // tensor cores: its second term, or null
   uint32_t* status;
   // tensor cores: no q_lat, o_lat in fp32, the partials [2 n_units, h, ...]
   PagedTcPlan tc;

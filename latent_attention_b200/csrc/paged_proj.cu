@@ -327,7 +327,7 @@ struct OutputParams {
   const float *part_o, *part_lse;          // [2 n_units, h, R], [2 n_units, h] (log2)
   const float* o_lat;                      // [B, h, R]: sequences in one segment
   const int64_t* pre;
-  __nv_bfloat16* out;                      // [B, h, dv]
+  __nv_bfloat16 *out, *out_lo;             // [B, h, dv]; what is left of it, or null
   int B, h, dn, dv, n_units, min_len, rounds;
   uint32_t* status;
 };
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant_
         }
       }
       // the second half's sums to the first
-      float* const at = sums + (lane >> 2) * PS + n0 + 2 * (lane & 3);
+      float* const to = sums + (lane >> 2) * PS + n0 + 2 * (lane & 3);
       if (kh == 1) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant_
           for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-              *reinterpret_cast<float2*>(at + (m * 16 + half * 8) * PS + q * 8) =
+              *reinterpret_cast<float2*>(to + (m * 16 + half * 8) * PS + q * 8) =
                   make_float2(acc[m][q][2 * half], acc[m][q][2 * half + 1]);
       }
       __syncthreads();
@@ -557,11 +557,17 @@ __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant_
               const int row = m * 16 + half * 8 + (lane >> 2);
               const int col = nc + n0 + q * 8 + 2 * (lane & 3);
               const float2 x =
-                  *reinterpret_cast<const float2*>(at + (m * 16 + half * 8) * PS + q * 8);
-              if (row < n && col < p.dv)
-                *reinterpret_cast<uint32_t*>(p.out + ((int64_t)(base + row) * p.h + hh) * p.dv +
-                                             col) =
-                    pack_bf16(acc[m][q][2 * half] + x.x, acc[m][q][2 * half + 1] + x.y);
+                  *reinterpret_cast<const float2*>(to + (m * 16 + half * 8) * PS + q * 8);
+              if (row < n && col < p.dv) {
+                const int64_t at = ((int64_t)(base + row) * p.h + hh) * p.dv + col;
+                const float y0 = acc[m][q][2 * half] + x.x, y1 = acc[m][q][2 * half + 1] + x.y;
+                const uint32_t hi = pack_bf16(y0, y1);
+                *reinterpret_cast<uint32_t*>(p.out + at) = hi;
+                if (p.out_lo)
+                  *reinterpret_cast<uint32_t*>(p.out_lo + at) =
+                      pack_bf16(y0 - __uint_as_float(hi << 16),
+                                y1 - __uint_as_float(hi & 0xffff0000u));
+              }
             }
       }
       __syncthreads();                     // sums and, past 128 columns, weights are read
@@ -610,7 +616,7 @@ cudaError_t launch_paged_output(const PagedDecodeArgs& a, int min_len, cudaStrea
   if (e != cudaSuccess) return e;
   OutputParams o;
   o.part_o = a.part_o; o.part_lse = a.part_lse; o.o_lat = (const float*)a.o_lat; o.pre = a.pre;
-  o.out = (__nv_bfloat16*)a.o;
+  o.out = (__nv_bfloat16*)a.o; o.out_lo = (__nv_bfloat16*)a.o_lo;
   o.B = a.B; o.h = a.h; o.dn = a.dn; o.dv = a.dv; o.n_units = a.tc.n_units; o.min_len = min_len;
   o.status = a.status;
   o.rounds = rounds_of(a);

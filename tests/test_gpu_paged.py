@@ -863,3 +863,18 @@ def test_append_refuses_a_second_run_among_many(cuda):
         idx = [slots[i] // 16 for i in ok]
         assert np.array_equal(sc[idx], wsc[idx])
         assert np.array_equal(O.E4M3[got[idx]], O.E4M3[want[idx]])
+
+
+@pytest.mark.parametrize("heads,hidden,B", [(1, 8, 1), (3, 136, 17), (16, 1000, 130), (128, 264, 5),
+                                            (5, 4096, 96), (40, 512, 300)])
+def test_decode_output_projection_shapes(cuda, heads, hidden, B):
+    """Tiles, pieces of K and batches that end inside a block."""
+    cfg = bf16(heads, hidden_size=hidden)
+    rng = np.random.default_rng(B)
+    check_decode(cfg, [int(x) for x in rng.integers(0, 60, B)], 16, seed=heads, with_o=True)
+
+
+def test_decode_other_widths_with_output_projection(cuda):
+    cfg = bf16(3, kv_lora_rank=96, qk_rope_head_dim=32, qk_nope_head_dim=24, v_head_dim=40,
+               hidden_size=120)
+    check_decode(cfg, [0, 70, 300], 32, seed=9, with_o=True)
