@@ -115,7 +115,7 @@ static_assert(smem_bytes<64>() <= 227 * 1024 && smem_bytes<48>() <= 227 * 1024 &
 struct AttnParams {
   const int64_t* pre;          // [B + 1] charged chunks
   const int32_t* len;          // [B] tokens
-  const int32_t* first;        // [n_units] sequence at the start of a slice
+  const int4* first;           // [n_units][2] a unit's first segment: b, c0, nch, slot; whole, tokens
   const int32_t* table;        // [B, max_blocks]
   const uint8_t* cache;
   const float* scales;
@@ -357,9 +357,20 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
   tc_fence_after();
   griddep_wait();
   griddep_launch_dependents();
-  const Slice sl = unit_slice(p.pre, p.B, u, p.n_units, p.min_len);
   Cursor c;                                   // (done at once where the slice is empty)
-  c.start(p.pre, p.B, sl, u, p.first[u]);
+  const int4 f0 = p.first[2 * u], f1 = p.first[2 * u + 1];
+  const int64_t total = p.pre[p.B];           // (the slice itself matters from the second segment on)
+  {
+    Seg s;
+    s.b = f0.x; s.c0 = f0.y; s.nch = f0.z; s.slot = f0.w;
+    s.whole = f1.x != 0;
+    c.resume(s);
+  }
+  const int n_first = f1.y;                   // tokens of its sequence
+  Slice sl;
+  sl.r0 = imin(u * slice_len(total, p.n_units, p.min_len), total);
+  sl.r1 = imin(sl.r0 + slice_len(total, p.n_units, p.min_len), total);
+  const auto tokens = [&](const Cursor& k) { return k.kk == 0 ? n_first : p.len[k.s.b]; };
   const auto advance = [&](Cursor& k) { k.next(p.pre, p.B, sl, u); };
 
   // TMA loads of box a of a chunk's `blocks` blocks (ids in shared memory); a
@@ -385,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
       int slot = 0, rs = 0, g = 0, n = 0;
       uint32_t ph = 1, rph = 1;               // parities of the empty barriers
       for (; !c.done; ++g) {
-        if (c.j == 0) n = p.len[c.s.b];
+        if (c.j == 0) n = tokens(c);
         const int valid = min(CT, n - (c.s.c0 + c.j) * CT);
         const int blocks = (valid + p.bs - 1) >> p.lbs;
         if (!mbar_wait(&sh.g_full[g % GR], (g / GR) & 1, abort_v, p.status)) break;
@@ -505,7 +516,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
     auto fetch = [&]() -> int {               // the id as the table has it; INT_MIN: no block
       int id = INT32_MIN;
       if (!look.done) {
-        if (look.j == 0) ln = p.len[look.s.b];
+        if (look.j == 0) ln = tokens(look);
         const int t = (look.s.c0 + look.j) * CT + lane * p.bs;
         if (lane < per_chunk && t < ln) {
           id = p.table[(int64_t)look.s.b * p.max_blocks + (t >> p.lbs)];
@@ -554,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
     int slot = 2;
     uint32_t ph = 1;
     for (int g = 0; !c.done; ++g) {
-      if (c.j == 0) n = p.len[c.s.b];
+      if (c.j == 0) n = tokens(c);
       const int valid = min(CT, n - (c.s.c0 + c.j) * CT);
       const int blocks = (valid + p.bs - 1) >> p.lbs;
       bool ok = true;
@@ -586,7 +597,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
     int g = 0;
     for (; !c.done; c.next_seg(p.pre, p.B, sl, u)) {
       const Seg s = c.s;
-      const int n = p.len[s.b];
+      const int n = tokens(c);
       if (tg < HPG) {
         sh.hf[h0 + tg] = p.qf[((int64_t)s.b * p.groups + hg) * NH + h0 + tg];
         sh.nref[h0 + tg] = 0.f;               // the first chunk sets it
@@ -797,15 +808,23 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
       // Segment end: row sums over the 128 tokens, then the output
       if (barrier_or(bar, 128, !ok)) break;
       {
-        float mine = 0.f;
+        // lanes trade halves of their heads until a lane has one
+        int head = 0;
 #pragma unroll
-        for (int i = 0; i < HPG; ++i) {
-          float x = l[i];
+        for (int w = HPG / 2, o = 16; o; w >>= 1, o >>= 1) {
+          if (w > 0) {
+            const bool up = lane & o;
+            head = 2 * head + up;
 #pragma unroll
-          for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          if (lane == i) mine = x;
+            for (int i = 0; i < w; ++i) {
+              const float give = up ? l[i] : l[i + w], mine = up ? l[i + w] : l[i];
+              l[i] = mine + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+          } else {
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+          }
         }
-        if (lane < HPG) sh.lsum[grp][quad][lane] = mine;
+        if (lane % (32 / HPG) == 0) sh.lsum[grp][quad][head] = l[0];
       }
       named_barrier_sync(bar, 128);
       if (lane < HPG) {
@@ -819,6 +838,9 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
       ok = warp_wait(&sh.o_done, c.kk & 1, abort_v, p.status);
       tc_fence_after();
       if (ok) {
+        float inv[HPG];
+#pragma unroll
+        for (int k = 0; k < HPG; ++k) inv[k] = sh.alpha[h0 + k];
 #pragma unroll 1
         for (int a = 0; a < 4; ++a) {
           uint32_t o[HPG], o2[HPG];
@@ -836,10 +858,9 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
                                 : p.part_o + ((int64_t)s.slot * p.h + head0) * R) + dim;
 #pragma unroll
           for (int k = 0; k < HPG; ++k) {
-            if (k >= n_heads) continue;
             float x = __uint_as_float(o[k]);
             if (K::STK) x += __uint_as_float(o2[k]);
-            dst[k * R] = x * sh.alpha[h0 + k];
+            if (k < n_heads) dst[k * R] = x * inv[k];
           }
         }
       }
@@ -897,7 +918,7 @@ cudaError_t tc_paged_decode(const PagedDecodeArgs& a, cudaStream_t st) {
       !encode_tmap(&tmCr, a.pool.cache, 2, cdims, str, crbox, 64))
     return cudaErrorInvalidValue;
   AttnParams p{};
-  p.pre = a.pre; p.len = a.len; p.first = a.first; p.table = a.table;
+  p.pre = a.pre; p.len = a.len; p.first = (const int4*)a.first; p.table = a.table;
   p.cache = a.pool.cache; p.scales = a.pool.scales; p.qf = a.qf;
   p.B = a.B; p.max_blocks = a.max_blocks; p.n_blocks = a.pool.n_blocks; p.bs = a.pool.bs;
   p.lbs = a.pool.bs == 16 ? 4 : a.pool.bs == 32 ? 5 : a.pool.bs == 64 ? 6 : 7;

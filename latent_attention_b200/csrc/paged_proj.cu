@@ -138,9 +138,16 @@ __device__ void lengths(const QueryParams& p) {
   }
   if (t == 0) p.pre[0] = 0;
   __syncthreads();
-  // the sequence at the start of every unit's slice
-  for (int u = t; u < p.n_units; u += NT)
-    p.first[u] = seq_at(p.pre, p.B, unit_slice(p.pre, p.B, u, p.n_units, p.min_len).r0);
+  // every unit's first segment: the attention kernel starts with one load
+  for (int u = t; u < p.n_units; u += NT) {
+    const Slice sl = unit_slice(p.pre, p.B, u, p.n_units, p.min_len);
+    Cursor c;
+    c.start(p.pre, p.B, sl, u, seq_at(p.pre, p.B, sl.r0));
+    int4* rec = reinterpret_cast<int4*>(p.first) + 2 * u;
+    const Seg& s = c.s;
+    rec[0] = c.done ? make_int4(0, 0, 0, 0) : make_int4(s.b, s.c0, s.nch, s.slot);
+    rec[1] = c.done ? make_int4(0, 0, 0, 0) : make_int4(s.whole, p.len[s.b], 0, 0);
+  }
 }
 
 // The 16-bit values that the four lanes of a quad hold of each of four groups

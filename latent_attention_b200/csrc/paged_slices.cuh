@@ -92,6 +92,12 @@ struct Cursor {
     if (sl.r0 >= sl.r1) { done = true; return; }
     seek(pre, B, sl, u, b);
   }
+  // the same from what start() found, kept by another kernel
+  MLA_PHD void resume(const Seg& first) {
+    kk = 0; j = 0;
+    s = first;
+    done = first.nch == 0;
+  }
   MLA_PHD void next_seg(const int64_t* pre, int B, const Slice& sl, int u) {
     j = 0; ++kk;
     seek(pre, B, sl, u, s.b + 1);
