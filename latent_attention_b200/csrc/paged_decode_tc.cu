@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
         ok = ok && warp_wait(&sh.e_full[g % GR], (g / GR) & 1, abort_v, p.status);
         const float sc = sh.scl[g % GR][row >> p.lbs];
         ok = ok && warp_wait(&sh.s_full[sls], (g / NSL) & 1, abort_v, p.status);
-        float v[HPG], pr[HPG], vm = -INFINITY;
+        float v[HPG], vm = -INFINITY;
         {
           uint32_t a[HPG], b[HPG];
           tc_fence_after();
@@ -661,42 +661,9 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
         }
         // the rare case: a score far above its reference (or a warp that gave up)
         const bool far = barrier_or(bar, 128, !ok || (live && vm > kGrow));
-        uint32_t m[HPG / 2];
-        int pair;                             // of heads whose maximum this lane ends with
-        bool leave = false;
-        for (bool checked = false;;) {
-#pragma unroll
-          for (int i = 0; i < HPG; ++i) pr[i] = ex2(v[i]);
-          // The largest p 2^e of the warp's 32 tokens per head, from the upper
-          // halves of the (non-negative) floats, whose order is that of their
-          // bits, NaN above all: lanes trade halves of their heads until a lane
-          // has two.
-#pragma unroll
-          for (int i = 0; i < HPG / 2; ++i) {
-            float x = pr[2 * i], y = pr[2 * i + 1];
-            mul2(x, y, sc, sc);
-            m[i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-          }
-          pair = 0;
-#pragma unroll
-          for (int w = HPG / 4, o = 16; o; w >>= 1, o >>= 1) {
-            if (w > 0) {
-              const bool up = lane & o;
-              pair = 2 * pair + up;
-#pragma unroll
-              for (int i = 0; i < w; ++i) {
-                const uint32_t give = up ? m[i] : m[i + w], mine = up ? m[i + w] : m[i];
-                m[i] = max_u16x2(mine, __shfl_xor_sync(0xffffffffu, give, o));
-              }
-            } else {
-              m[0] = max_u16x2(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
-            }
-          }
-          if (checked) break;
-          checked = true;
-          if (!far) break;
+        if (far) {
           // new references; if a warp gave up, the group leaves together
-          if (barrier_or(bar, 128, !ok)) { leave = true; break; }
+          if (barrier_or(bar, 128, !ok)) { ok = false; break; }
           int mine = 0;
 #pragma unroll
           for (int i = 0; i < HPG; ++i) {
@@ -741,49 +708,69 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
 #pragma unroll
           for (int i = 0; i < HPG; ++i) v[i] += sh.nref[h0 + i];
         }
-        if (leave) { ok = false; break; }
+        // p, its row sums, and p 2^e
+        uint32_t m[HPG / 2];
+#pragma unroll
+        for (int i = 0; i < HPG; i += 2) {
+          v[i] = ex2(v[i]);
+          v[i + 1] = ex2(v[i + 1]);
+          add2(l[i], l[i + 1], v[i], v[i + 1]);
+          mul2(v[i], v[i + 1], sc, sc);
+          m[i / 2] = __byte_perm(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), 0x7632);
+        }
+        // The largest of the warp's 32 tokens per head, from the upper halves of
+        // the (non-negative) floats, whose order is that of their bits, NaN above
+        // all: lanes trade halves of their heads until a lane has two.  (A
+        // redux.sync per head, 16 one after the other, took 8 % longer.)
+        int pair = 0;
+#pragma unroll
+        for (int w = HPG / 4, o = 16; o; w >>= 1, o >>= 1) {
+          if (w > 0) {
+            const bool up = lane & o;
+            pair = 2 * pair + up;
+#pragma unroll
+            for (int i = 0; i < w; ++i) {
+              const uint32_t give = up ? m[i] : m[i + w], mine = up ? m[i + w] : m[i];
+              m[i] = max_u16x2(mine, __shfl_xor_sync(0xffffffffu, give, o));
+            }
+          } else {
+            m[0] = max_u16x2(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+          }
+        }
+        // it goes to [128, 256): factor 2^-k, and the scale 2^k as a ue8m0 byte
+        const uint32_t ex0 = max(m[0] & 0x7f80u, 8u << 7) << 16;
+        const uint32_t ex1 = max((m[0] >> 16) & 0x7f80u, 8u << 7) << 16;
+        constexpr int SAME = 64 / HPG;        // lanes with the same pair
+        if (lane % SAME == 0)
+          *reinterpret_cast<float2*>(inv_w + 2 * pair) =
+              make_float2(__uint_as_float(0x82800000u - ex0), __uint_as_float(0x82800000u - ex1));
+        __syncwarp();
+        uint32_t hb[HPG / 4], lb[HPG / 4];
+#pragma unroll
+        for (int i = 0; i < HPG / 4; ++i) {
+          const float4 f = *reinterpret_cast<const float4*>(inv_w + 4 * i);
+          float* const w = v + 4 * i;
+          mul2(w[0], w[1], f.x, f.y);
+          mul2(w[2], w[3], f.z, f.w);
+          const uint32_t w01 = pack_f16(w[0], w[1]), w23 = pack_f16(w[2], w[3]);
+          const uint32_t h01 = f16x2_to_e4m3x2(w01), h23 = f16x2_to_e4m3x2(w23);
+          hb[i] = h01 | (h23 << 16);
+          lb[i] = f16x2_to_e4m3x2(sub_f16x2(w01, e4m3x2_to_f16x2(h01))) |
+                  (f16x2_to_e4m3x2(sub_f16x2(w23, e4m3x2_to_f16x2(h23))) << 16);
+        }
         // PV of chunk g - NP has run: this P buffer and its scales are free
         if (g >= NP) ok = ok && warp_wait(&sh.pv_done[pb], ((g / NP) - 1) & 1, abort_v, p.status);
-        // the largest goes to [128, 256): factor 2^-k, and the scale 2^k as a
-        // ue8m0 byte
-        constexpr int SAME = 64 / HPG;        // lanes with the same pair
         if (lane % SAME == 0) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t ex = max((k ? m[0] >> 16 : m[0] & 0xffffu) & 0x7f80u, 8u << 7) << 16;
-            inv_w[2 * pair + k] = __uint_as_float(0x82800000u - ex);
             const int nh = h0 + 2 * pair + k;
-            const uint8_t sfb = (uint8_t)((ex >> 23) - 7);
+            const uint8_t sfb = (uint8_t)(((k ? ex1 : ex0) >> 23) - 7);
             sh.sf[pb][(nh & 31) * 16 + (nh >> 5) * 4 + quad] = sfb;
             if (K::STK) sh.sf[pb][((nh + NH) & 31) * 16 + ((nh + NH) >> 5) * 4 + quad] = sfb;
           }
         }
-        __syncwarp();
         const uint32_t pt = p_base + pb * K::PBYTES;
         constexpr uint32_t lo_at = K::STK ? NH : 0, lo_tile = K::STK ? 0 : CT * 64;
-        uint32_t hb[HPG / 4], lb[HPG / 4];
-#pragma unroll
-        for (int i = 0; i < HPG; i += 8) {
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float4 f = *reinterpret_cast<const float4*>(inv_w + i + 4 * q);
-            mul2(f.x, f.y, sc, sc);
-            mul2(f.z, f.w, sc, sc);
-            float* const w = pr + i + 4 * q;
-            add2(l[i + 4 * q], l[i + 4 * q + 1], w[0], w[1]);
-            add2(l[i + 4 * q + 2], l[i + 4 * q + 3], w[2], w[3]);
-            mul2(w[0], w[1], f.x, f.y);
-            mul2(w[2], w[3], f.z, f.w);
-            const uint32_t w01 = pack_f16(w[0], w[1]), w23 = pack_f16(w[2], w[3]);
-            const uint32_t h01 = f16x2_to_e4m3x2(w01), h23 = f16x2_to_e4m3x2(w23);
-            hi[q] = h01 | (h23 << 16);
-            lo[q] = f16x2_to_e4m3x2(sub_f16x2(w01, e4m3x2_to_f16x2(h01))) |
-                    (f16x2_to_e4m3x2(sub_f16x2(w23, e4m3x2_to_f16x2(h23))) << 16);
-          }
-          hb[i / 4] = hi[0]; hb[i / 4 + 1] = hi[1];
-          lb[i / 4] = lo[0]; lb[i / 4 + 1] = lo[1];
-        }
         const uint32_t at = row * K::PW + h0;
         if constexpr (HPG == 16) {
           st_shared_v4(pt + swz<K::PW>(at), hb[0], hb[1], hb[2], hb[3]);
