@@ -86,7 +86,7 @@ void paged_layout(const mla_config& c, int B, int max_blocks, int block_size,
     parts = L->max_splits;
     L->q_lat = -1;
     L->q8 = take(rows * 2 * w + rows * 4);     // the terms, then a factor per row
-    L->plan = take(32 * (int64_t)t.n_units + ((int64_t)B + 1) * 8 + (int64_t)B * 4);
+    L->plan = take(32 * (int64_t)t.n_units + ((int64_t)B + 1) * 8 + (int64_t)B * 12);
   } else {
     L->split_tokens = simt_split(c, B, max_ctx);
     L->max_splits = (int32_t)((max_ctx + L->split_tokens - 1) / L->split_tokens);
@@ -285,7 +285,8 @@ mla_status mla_decode_paged(const mla_config* cfg, const void* q_nope, const voi
     a.qf = (float*)(a.q8 + rows * 2 * (a.r + a.dr));
     a.first = (int32_t*)(ws + L.plan);
     a.pre = (int64_t*)(a.first + 8 * (int64_t)a.tc.n_units);
-    a.len = (int32_t*)(a.pre + B + 1);
+    a.parts = (int32_t*)(a.pre + B + 1);
+    a.len = a.parts + 2 * (int64_t)B;
     e = mla::tc_paged_decode(a, st);
   } else {
     e = mla::launch_paged_decode_simt(c.dtype, a, st);

@@ -177,7 +177,7 @@ struct PagedDecodeArgs {
   uint8_t* q8;                     // [B, groups, 2, NH, r + dr] e4m3 terms
   float* qf;                       // [B, groups, NH]
   int64_t* pre;                    // [B + 1]
-  int32_t *len, *first;            // [B]; [n_units][8] a unit's first segment
+  int32_t *len, *first, *parts;    // [B]; [n_units][8] a unit's first segment; [B][2] partials
 };
 
 // cudaFuncSetAttribute applies to the current device only: set a kernel's

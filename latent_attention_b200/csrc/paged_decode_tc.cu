@@ -921,7 +921,7 @@ cudaError_t tc_paged_decode(const PagedDecodeArgs& a, cudaStream_t st) {
   count_launches();
   if (e != cudaSuccess) return e;
   stage_event(2, st);
-  e = launch_paged_output(a, p.min_len, st);
+  e = launch_paged_output(a, st);
   if (e != cudaSuccess) return e;
   stage_event(3, st);
   return cudaGetLastError();

@@ -10,10 +10,11 @@
 // Both read each head's 128 KB of weights once and do little with them (a
 // decode batch has tens of rows): what bounds them is the time of a launch, of
 // one trip to memory and of fetching their instructions, so the work around
-// the products (rounding to 8 bits, merging) is done where the operands are,
-// and the products are warp-level MMAs on shared memory, whose results the
-// threads hold in registers; a tcgen05 product would have to be read back out
-// of TMEM first.  (Four blocks a head, in a cluster, took longer: 45 us
+// the products (rounding to 8 bits, merging) is done where the operands are.
+// The query's product is warp-level MMAs, whose results the threads round where
+// they hold them, a row of q_lat in one warp's quads; the output's is tcgen05
+// with the 128 columns as M and the sequences as N (as warp-level MMAs, some 19
+// cycles each, it took 5000 cycles of 12500 for 16 sequences).  (Four blocks a head, in a cluster, took longer: 45 us
 // against 26 at 64 sequences of 128 heads.)  Neither q_lat nor o_lat is rounded
 // to 16 bits: q_lat goes from fp32 to its two terms, o_lat enters the product as
 // two bf16 terms (16 significant bits).
@@ -78,6 +79,7 @@ struct QueryParams {
   const int32_t* ctx;
   int64_t* pre;
   int32_t *len, *first;
+  int2* parts;
   int B, h, dn, dv, groups, hg_heads, NH, n_units, min_len, rounds;
   int64_t most;                            // tokens a table holds
   float scale_log2;
@@ -138,6 +140,17 @@ __device__ void lengths(const QueryParams& p) {
   }
   if (t == 0) p.pre[0] = 0;
   __syncthreads();
+  // every sequence's partial results: the slot of the first, their number (1:
+  // the whole sequence, not in a slot; 0: no tokens).  The others' slots are
+  // those of the next units' first segments.
+  for (int b = t; b < p.B; b += NT) {
+    int2 x = make_int2(0, 0);
+    if (p.len[b] > 0) {
+      const SeqUnits su = seq_units(p.pre, b, p.B, p.n_units, p.min_len);
+      x = make_int2(seq_slot(su, su.u0), su.u1 - su.u0 + 1);
+    }
+    p.parts[b] = x;
+  }
   // every unit's first segment: the attention kernel starts with one load
   for (int u = t; u < p.n_units; u += NT) {
     const Slice sl = unit_slice(p.pre, p.B, u, p.n_units, p.min_len);
@@ -252,26 +265,30 @@ __global__ void __launch_bounds__(NT) paged_query_kernel(const __grid_constant__
         uint32_t a[2][4], b[2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
-          ldsm4(qbase + (ks >> 2) * (Q_TILE / 2) +
-                    box_at(m * 16 + (lane & 15), 2 * (ks & 3) + (lane >> 4)), a[m]);
+          if (m == 0 || n > 16)
+            ldsm4(qbase + (ks >> 2) * (Q_TILE / 2) +
+                      box_at(m * 16 + (lane & 15), 2 * (ks & 3) + (lane >> 4)), a[m]);
 #pragma unroll
         for (int q = 0; q < 2; ++q)
           ldsm4_t(wbase + (warp >> 1) * WBOX +
                       box_at(ks * 16 + (lane & 15), 4 * (warp & 1) + 2 * q + (lane >> 4)), b[q]);
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m) {
+          if (m == 1 && n <= 16) continue;
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             mma16816(acc[m][2 * q], a[m], b[q][0], b[q][1]);
             mma16816(acc[m][2 * q + 1], a[m], b[q][2], b[q][3]);
           }
+        }
       }
       __syncthreads();                     // weights and q are read
     }
     // the rows' maxima
     uint32_t* amax = amax_s[round & 1];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 2; ++m) {
+      if (m == 1 && n <= 16) continue;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t y = 0;
@@ -282,6 +299,7 @@ __global__ void __launch_bounds__(NT) paged_query_kernel(const __grid_constant__
         y = max(y, __shfl_xor_sync(0xffffffffu, y, 2));
         if ((lane & 3) == 0) atomicMax(&amax[m * 16 + half * 8 + r], y);
       }
+    }
     float pe[4] = {__uint_as_float(pe2.x << 16), __uint_as_float(pe2.x & 0xffff0000u),
                    __uint_as_float(pe2.y << 16), __uint_as_float(pe2.y & 0xffff0000u)};
     {
@@ -295,7 +313,7 @@ __global__ void __launch_bounds__(NT) paged_query_kernel(const __grid_constant__
     __syncthreads();
     if (t < MB) amax_s[~round & 1][t] = 0;  // for the next round (its barriers lie between)
 #pragma unroll 1
-    for (int mh = 0; mh < 4; ++mh) {
+    for (int mh = 0; mh < (n > 16 ? 4 : 2); ++mh) {
       const int row = (mh >> 1) * 16 + (mh & 1) * 8 + r;
       const float f = pow2(-scale_exp(amax[row]));
       uint32_t hi[4], lo[4];
@@ -333,35 +351,52 @@ __global__ void __launch_bounds__(NT) paged_query_kernel(const __grid_constant__
 struct OutputParams {
   const float *part_o, *part_lse;          // [2 n_units, h, R], [2 n_units, h] (log2)
   const float* o_lat;                      // [B, h, R]: sequences in one segment
-  const int64_t* pre;
+  const int2* parts;                       // [B] slot of the first partial, their number
   __nv_bfloat16 *out, *out_lo;             // [B, h, dv]; what is left of it, or null
-  int B, h, dn, dv, n_units, min_len, rounds;
+  int B, h, dn, dv, rounds;
   uint32_t* status;
 };
 constexpr int A_BYTES = 8 * MB * 128;      // o_lat of 32 sequences, one bf16 term
-constexpr int PS = 132;                    // floats of a row of the sums (128, padded)
-constexpr int O_SUMS = MB * PS * 4;        // (also 8 rows of 512: the merge of many partials)
-static_assert(O_SUMS >= 8 * R * 4, "sums");
-constexpr int O_SMEM = W_BYTES + 2 * A_BYTES + O_SUMS + 1024;
+constexpr int RED = 8 * R * 4;             // the merge of many partials
+constexpr int O_SMEM = W_BYTES + 2 * A_BYTES + RED + 1024;
 constexpr int kUnits = 512;                // most units (host side: tc_paged_plan)
 constexpr int kShared = 8;                 // more partials than this: the whole block merges
+
+// D (+)= A B^T; the weights A stay in the collector for the second term.
+template <bool LAST>
+__device__ __forceinline__ void mma_keep(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t acc) {
+  if (LAST)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16.collector::a::lastuse [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16.collector::a::fill [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
 
 __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant__ CUtensorMap tmW,
                                                           OutputParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full;
+  __shared__ __align__(8) uint64_t full, done;
   __shared__ int abort_flag;
+  __shared__ uint32_t tmem_base;
   __shared__ uint32_t many;                // rows that the whole block merges
   __shared__ const float* src_s[MB][kShared];   // a row's partials
   __shared__ float w_s[MB][kShared];       // and their weights
+  __shared__ float u_s[2 * kUnits];        // lse and weights of one row with many partials
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int hh = blockIdx.x;
   const int b0 = blockIdx.y * MB * p.rounds, nb = min(MB * p.rounds, p.B - b0);
   const uint32_t wbase = smem_u32(smem), abase = wbase + W_BYTES;
-  float* sums = reinterpret_cast<float*>(smem + W_BYTES + 2 * A_BYTES);
-  __shared__ float u_s[2 * kUnits];        // lse and weights of one row with many partials
+  float* red = reinterpret_cast<float*>(smem + W_BYTES + 2 * A_BYTES);
   auto load_w = [&](int nc) {
     mbar_arrive_expect_tx(&full, W_BYTES);
     for (int i = 0; i < 8; ++i)
@@ -369,6 +404,7 @@ __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant_
   };
   if (t == 0) {
     mbar_init(&full, 1);
+    mbar_init(&done, 1);
     abort_flag = 0;
     fence_barrier_init();
     // The weights do not depend on the kernel before this one (which started
@@ -376,11 +412,17 @@ __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant_
     // ends.
     load_w(0);
   }
+  if (warp == 1) {
+    tmem_alloc(&tmem_base, 32);
+    tc_fence_before();
+  }
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = tmem_base;
   griddep_wait();
   griddep_launch_dependents();
 
-  // four dims of a row as two bf16 terms into the A operand's boxes
+  // four dims of a row as two bf16 terms into the B operand's boxes
   auto put = [&](int row, int d, const float4& v) {
     const uint32_t h0 = pack_bf16(v.x, v.y), h1 = pack_bf16(v.z, v.w);
     const uint32_t l0 = pack_bf16(v.x - __uint_as_float(h0 << 16),
@@ -391,81 +433,82 @@ __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant_
     *reinterpret_cast<uint2*>(at) = make_uint2(h0, h1);
     *reinterpret_cast<uint2*>(at + A_BYTES) = make_uint2(l0, l1);
   };
-  int phase = 0;
+  // slot of partial i of a sequence
+  auto slot_of = [](const int2& x, int i) { return i == 0 ? x.x : 2 * ((x.x >> 1) + i); };
+  int phase = 0, runs = 0;
   bool coming = true;                      // weights are on their way
   for (int round = 0; round * MB < nb; ++round) {
     const int base = b0 + round * MB, n = min(MB, nb - round * MB);
+    const int rows = n <= 16 ? 16 : 32;    // N of the product
     if (t == 0) many = 0;
     __syncthreads();
-    // a thread per row: where its partial results lie, and their weights
-    if (t < MB) {
-      const int b = base + t;
-#pragma unroll
-      for (int i = 0; i < kShared; ++i) src_s[t][i] = nullptr;
-      if (t < n && p.pre[b + 1] != p.pre[b]) {
-        const SeqUnits su = seq_units(p.pre, b, p.B, p.n_units, p.min_len);
-        if (su.u0 == su.u1) {
-          src_s[t][0] = p.o_lat + ((int64_t)b * p.h + hh) * R;
-          w_s[t][0] = 1.f;
-        } else if (su.u1 - su.u0 < kShared) {
-          float mx = -INFINITY, den = 0.f, lse[kShared];
-#pragma unroll
-          for (int i = 0; i < kShared; ++i) {
-            lse[i] = su.u0 + i <= su.u1
-                         ? p.part_lse[(int64_t)seq_slot(su, su.u0 + i) * p.h + hh] : -INFINITY;
-            mx = fmaxf(mx, lse[i]);
-          }
-#pragma unroll
-          for (int i = 0; i < kShared; ++i) {
-            lse[i] = su.u0 + i <= su.u1 ? exp2f(lse[i] - mx) : 0.f;
-            den += lse[i];
-          }
-#pragma unroll
-          for (int i = 0; i < kShared; ++i)
-            if (su.u0 + i <= su.u1) {
-              src_s[t][i] = p.part_o + ((int64_t)seq_slot(su, su.u0 + i) * p.h + hh) * R;
-              w_s[t][i] = lse[i] / den;
-            }
-        } else {
-          atomicOr(&many, 1u << t);
-        }
+    // a thread per row and partial: where it lies, and its weight
+    if (t < MB * kShared) {
+      const int row = t / kShared, i = t % kShared, b = base + row;
+      const int2 x = row < n ? p.parts[b] : make_int2(0, 0);
+      const float* src = nullptr;
+      float w = 1.f;
+      if (x.y == 1) {
+        if (i == 0) src = p.o_lat + ((int64_t)b * p.h + hh) * R;
+      } else if (x.y > kShared) {
+        if (i == 0) atomicOr(&many, 1u << row);
+      } else if (i < x.y) {
+        const int64_t at = (int64_t)slot_of(x, i) * p.h + hh;
+        src = p.part_o + at * R;
+        w = p.part_lse[at];
       }
+      // (eight neighbouring lanes hold a row)
+      const bool part = x.y > 1 && x.y <= kShared && i < x.y;
+      float mx = part ? w : -INFINITY;
+#pragma unroll
+      for (int o = 1; o < kShared; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      if (part) w = exp2f(w - mx);
+      float den = part ? w : 0.f;
+#pragma unroll
+      for (int o = 1; o < kShared; o <<= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+      src_s[row][i] = src;
+      w_s[row][i] = part ? w / den : 1.f;
     }
     __syncthreads();
 #pragma unroll 1
-    for (int row = warp; row < MB; row += NT / 32) {
+    for (int row = warp; row < rows; row += NT / 32) {
       float4 v[4];
-      const float* src = src_s[row][0];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      // two partials (32 bytes a lane and 128 dims) in flight
 #pragma unroll 1
-      for (int i = 0; src; src = ++i < kShared ? src_s[row][i] : nullptr) {
-        const float w = w_s[row][i];
-        float4 x[4];
+      for (int i = 0; i < kShared && src_s[row][i]; i += 2) {
+        const float *s0 = src_s[row][i], *s1 = src_s[row][i + 1];
+        const float w0 = w_s[row][i], w1 = w_s[row][i + 1];
+        float4 x[4], y[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[q] = reinterpret_cast<const float4*>(src)[lane + 32 * q];
+        for (int q = 0; q < 4; ++q) x[q] = reinterpret_cast<const float4*>(s0)[lane + 32 * q];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          y[q] = s1 ? reinterpret_cast<const float4*>(s1)[lane + 32 * q]
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          v[q].x = fmaf(w, x[q].x, v[q].x); v[q].y = fmaf(w, x[q].y, v[q].y);
-          v[q].z = fmaf(w, x[q].z, v[q].z); v[q].w = fmaf(w, x[q].w, v[q].w);
+          v[q].x = fmaf(w1, y[q].x, fmaf(w0, x[q].x, v[q].x));
+          v[q].y = fmaf(w1, y[q].y, fmaf(w0, x[q].y, v[q].y));
+          v[q].z = fmaf(w1, y[q].z, fmaf(w0, x[q].z, v[q].z));
+          v[q].w = fmaf(w1, y[q].w, fmaf(w0, x[q].w, v[q].w));
         }
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) put(row, 4 * lane + 128 * q, v[q]);
     }
     for (uint32_t left = many; left; left &= left - 1) {
-      const int row = __ffs(left) - 1, b = base + row;
-      const SeqUnits su = seq_units(p.pre, b, p.B, p.n_units, p.min_len);
-      const int nu = su.u1 - su.u0 + 1;    // at most kUnits
+      const int row = __ffs(left) - 1;
+      const int2 x = p.parts[base + row];  // (at most kUnits partials)
       float mx = -INFINITY, den = 0.f;
       __syncthreads();
-      for (int i = t; i < nu; i += NT)
-        u_s[i] = p.part_lse[(int64_t)seq_slot(su, su.u0 + i) * p.h + hh];
+      for (int i = t; i < x.y; i += NT) u_s[i] = p.part_lse[(int64_t)slot_of(x, i) * p.h + hh];
       __syncthreads();
-      for (int i = lane; i < nu; i += 32) mx = fmaxf(mx, u_s[i]);
+      for (int i = lane; i < x.y; i += 32) mx = fmaxf(mx, u_s[i]);
 #pragma unroll
       for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      for (int i = t; i < nu; i += NT) u_s[kUnits + i] = exp2f(u_s[i] - mx);
+      for (int i = t; i < x.y; i += NT) u_s[kUnits + i] = exp2f(u_s[i] - mx);
       __syncthreads();
       // every eighth partial and half of the dims a warp
       float4 v[2];
@@ -473,36 +516,39 @@ __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant_
       for (int q = 0; q < 2; ++q) v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
       const int at = lane + 64 * (warp >> 3);
 #pragma unroll 4
-      for (int i = warp & 7; i < nu; i += 8) {
-        const float4* src = reinterpret_cast<const float4*>(
-            p.part_o + ((int64_t)seq_slot(su, su.u0 + i) * p.h + hh) * R);
+      for (int i = warp & 7; i < x.y; i += 8) {
+        const float4* src =
+            reinterpret_cast<const float4*>(p.part_o + ((int64_t)slot_of(x, i) * p.h + hh) * R);
         const float w = u_s[kUnits + i];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const float4 x = src[at + 32 * q];
-          v[q].x = fmaf(w, x.x, v[q].x); v[q].y = fmaf(w, x.y, v[q].y);
-          v[q].z = fmaf(w, x.z, v[q].z); v[q].w = fmaf(w, x.w, v[q].w);
+          const float4 y = src[at + 32 * q];
+          v[q].x = fmaf(w, y.x, v[q].x); v[q].y = fmaf(w, y.y, v[q].y);
+          v[q].z = fmaf(w, y.z, v[q].z); v[q].w = fmaf(w, y.w, v[q].w);
         }
       }
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        reinterpret_cast<float4*>(sums + (warp & 7) * R)[at + 32 * q] = v[q];
-      for (int i = lane; i < nu; i += 32) den += u_s[kUnits + i];
+        reinterpret_cast<float4*>(red + (warp & 7) * R)[at + 32 * q] = v[q];
+      for (int i = lane; i < x.y; i += 32) den += u_s[kUnits + i];
 #pragma unroll
       for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
       __syncthreads();
       if (t < R / 4) {
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int w = 0; w < 8; ++w) {
-          const float4 x = reinterpret_cast<const float4*>(sums + w * R)[t];
-          y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+          const float4 z = reinterpret_cast<const float4*>(red + w * R)[t];
+          y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
         }
         const float inv = 1.f / den;
         y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
         put(row, 4 * t, y);
       }
     }
+    fence_proxy_async();                   // the operand's boxes, to the tensor core
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
     // up to 128 output columns the weights stay for all rounds
     for (int nc = 0; nc < p.dv; nc += 128) {
       if (!coming && p.dv > 128) {
@@ -512,74 +558,59 @@ __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant_
       // (after a timeout the block goes on; the status word says so)
       if (coming) mbar_wait(&full, phase++ & 1, &abort_flag, p.status);
       coming = false;
-      // a warp: 16 columns, half of the dims
-      const int n0 = (warp & 7) * 16, kh = warp >> 3;
-      float acc[2][2][4];
+      // the columns as M, the sequences as N
+      if (warp == 0 && elect_one()) {
+        const uint32_t idesc = idesc_bf16(128, rows);
+#pragma unroll 1
+        for (int box = 0; box < 8; ++box) {
+          const uint64_t da = desc_kmajor_sw128(wbase + box * WBOX);
+          const uint64_t dh = desc_kmajor_sw128(abase + box * MB * 128);
+          const uint64_t dl = desc_kmajor_sw128(abase + A_BYTES + box * MB * 128);
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+          for (int k = 0; k < 4; ++k) {
+            mma_keep<false>(tbase, da + 2 * k, dh + 2 * k, idesc, (box | k) != 0);
+            mma_keep<true>(tbase, da + 2 * k, dl + 2 * k, idesc, 1);
+          }
+        }
+        mma_commit(&done);
+      }
+      __syncwarp();
+      mbar_wait(&done, runs++ & 1, &abort_flag, p.status);
+      tc_fence_after();
+      __syncthreads();                     // (the warps reconverge before the TMEM loads)
+      if (warp < 8 && nc + (warp & 3) * 32 < p.dv) {
+        // a warp: 32 columns of 16 sequences
+        const int half = warp >> 2, col = nc + (warp & 3) * 32 + lane;
+        if (16 * half < n) {
+          uint32_t v[16];
+          asm volatile(
+              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+              "%10, %11, %12, %13, %14, %15}, [%16];"
+              : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]),
+                "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+              : "r"(tbase + ((uint32_t)((warp & 3) * 32) << 16) + 16 * half));
+          tmem_wait_ld();
+          if (col < p.dv) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[m][q][k] = 0.f;
-#pragma unroll 2
-      for (int ks = 16 * kh; ks < 16 * kh + 16; ++ks) {
-        const int box = ks >> 2, c = 2 * (ks & 3);
-        uint32_t b[4];
-        ldsm4(wbase + box * WBOX +
-                  box_at(n0 + (lane & 7) + ((lane >> 4) & 1) * 8, c + ((lane >> 3) & 1)), b);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if (m * 16 >= n) continue;
-          const uint32_t at =
-              abase + box * MB * 128 + box_at(m * 16 + (lane & 15), c + (lane >> 4));
-          uint32_t hi[4], lo[4];
-          ldsm4(at, hi);
-          ldsm4(at + A_BYTES, lo);
-          mma16816(acc[m][0], lo, b[0], b[1]);
-          mma16816(acc[m][1], lo, b[2], b[3]);
-          mma16816(acc[m][0], hi, b[0], b[1]);
-          mma16816(acc[m][1], hi, b[2], b[3]);
+            for (int k = 0; k < 16; ++k) {
+              const int row = 16 * half + k;
+              if (row >= n) break;
+              const int64_t at = ((int64_t)(base + row) * p.h + hh) * p.dv + col;
+              const float x = __uint_as_float(v[k]);
+              const __nv_bfloat16 hi = __float2bfloat16(x);
+              p.out[at] = hi;
+              if (p.out_lo) p.out_lo[at] = __float2bfloat16(x - __bfloat162float(hi));
+            }
+          }
         }
       }
-      // the second half's sums to the first
-      float* const to = sums + (lane >> 2) * PS + n0 + 2 * (lane & 3);
-      if (kh == 1) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-              *reinterpret_cast<float2*>(to + (m * 16 + half * 8) * PS + q * 8) =
-                  make_float2(acc[m][q][2 * half], acc[m][q][2 * half + 1]);
-      }
-      __syncthreads();
-      if (kh == 0) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int row = m * 16 + half * 8 + (lane >> 2);
-              const int col = nc + n0 + q * 8 + 2 * (lane & 3);
-              const float2 x =
-                  *reinterpret_cast<const float2*>(to + (m * 16 + half * 8) * PS + q * 8);
-              if (row < n && col < p.dv) {
-                const int64_t at = ((int64_t)(base + row) * p.h + hh) * p.dv + col;
-                const float y0 = acc[m][q][2 * half] + x.x, y1 = acc[m][q][2 * half + 1] + x.y;
-                const uint32_t hi = pack_bf16(y0, y1);
-                *reinterpret_cast<uint32_t*>(p.out + at) = hi;
-                if (p.out_lo)
-                  *reinterpret_cast<uint32_t*>(p.out_lo + at) =
-                      pack_bf16(y0 - __uint_as_float(hi << 16),
-                                y1 - __uint_as_float(hi & 0xffff0000u));
-              }
-            }
-      }
-      __syncthreads();                     // sums and, past 128 columns, weights are read
+      tc_fence_before();
+      __syncthreads();                     // TMEM and, past 128 columns, weights are read
+      tc_fence_after();
     }
   }
+  if (warp == 1) tmem_dealloc(tbase, 32);
 }
 
 // W_UK and W_UV rows of all heads, boxes of 128 rows x 64 columns.
@@ -603,7 +634,7 @@ cudaError_t launch_paged_query(const PagedDecodeArgs& a, int min_len, cudaStream
   q.q8 = a.q8; q.qf = a.qf; q.ctx = a.ctx; q.pre = a.pre; q.len = a.len;
   q.B = a.B; q.h = a.h; q.dn = a.dn; q.dv = a.dv;
   q.groups = a.tc.groups; q.hg_heads = a.tc.hg_heads; q.NH = a.tc.NH;
-  q.first = a.first; q.n_units = a.tc.n_units; q.min_len = min_len;
+  q.first = a.first; q.parts = (int2*)a.parts; q.n_units = a.tc.n_units; q.min_len = min_len;
   q.most = (int64_t)a.max_blocks * a.pool.bs;
   q.scale_log2 = a.scale * 1.4426950408889634f;
   q.status = a.status;
@@ -615,16 +646,17 @@ cudaError_t launch_paged_query(const PagedDecodeArgs& a, int min_len, cudaStream
                     st, tmW, q);
 }
 
-cudaError_t launch_paged_output(const PagedDecodeArgs& a, int min_len, cudaStream_t st) {
+cudaError_t launch_paged_output(const PagedDecodeArgs& a, cudaStream_t st) {
   CUtensorMap tmW;
   if (!weight_map(&tmW, a)) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> set{0};
   const cudaError_t e = set_dynamic_smem((const void*)paged_output_kernel, O_SMEM, set);
   if (e != cudaSuccess) return e;
   OutputParams o;
-  o.part_o = a.part_o; o.part_lse = a.part_lse; o.o_lat = (const float*)a.o_lat; o.pre = a.pre;
+  o.part_o = a.part_o; o.part_lse = a.part_lse; o.o_lat = (const float*)a.o_lat;
+  o.parts = (const int2*)a.parts;
   o.out = (__nv_bfloat16*)a.o; o.out_lo = (__nv_bfloat16*)a.o_lo;
-  o.B = a.B; o.h = a.h; o.dn = a.dn; o.dv = a.dv; o.n_units = a.tc.n_units; o.min_len = min_len;
+  o.B = a.B; o.h = a.h; o.dn = a.dn; o.dv = a.dv;
   o.status = a.status;
   o.rounds = rounds_of(a);
   count_launches();

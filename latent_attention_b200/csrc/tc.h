@@ -25,7 +25,7 @@ PagedTcPlan tc_paged_plan(int h, int sms);
 cudaError_t tc_paged_decode(const PagedDecodeArgs& a, cudaStream_t st);
 // Its projections: query (and lengths, status word), output.
 cudaError_t launch_paged_query(const PagedDecodeArgs& a, int min_len, cudaStream_t st);
-cudaError_t launch_paged_output(const PagedDecodeArgs& a, int min_len, cudaStream_t st);
+cudaError_t launch_paged_output(const PagedDecodeArgs& a, cudaStream_t st);
 // out [B, hidden] = (o + o_lo) [B, K] w_o [hidden, K]^T.
 bool tc_paged_oproj_supported(const mla_config& c);
 cudaError_t launch_paged_oproj(const void* o, const void* o_lo, const void* w_o, void* out, int B,
