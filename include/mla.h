@@ -378,9 +378,10 @@ MLA_API mla_status mla_decode_absorbed(const mla_config* cfg, const void* q_nope
  *
  * Lengths, block ids, slots and scales are read on the device only.  One that
  * is out of range never leads outside a buffer: it is replaced or skipped and
- * the status word says so (mla_check_device_status: MLA_ERR_SHAPE).  Calls on
- * one workspace share its status word and scratch: calls that may overlap on
- * the GPU need workspaces of their own.
+ * the status word says so (mla_check_device_status: MLA_ERR_SHAPE); a scale
+ * that is not such a power of two is read as 1.  Calls on one workspace share
+ * its status word and scratch: calls that may overlap on the GPU need
+ * workspaces of their own.
  */
 
 /* Workspace bytes of mla_paged_plan, _append and _gather on a pool of
@@ -442,7 +443,8 @@ MLA_API mla_status mla_paged_plan(const int32_t* ctx_len, const int32_t* new_len
  * and the run's rows e4m3(v * 2^-e), to nearest, ties to even.  An infinity or
  * NaN becomes NaN.  Rows of the block behind the run are not touched, and are
  * dead: write a block front to back.
- * A slot outside the pool, a slot in the block of the slot before it that does
+ * In front of a run, a block whose scale is not a power of two keeps its bytes
+ * and is reported.  A slot outside the pool, a slot in the block of the slot before it that does
  * not follow it, and a second run in one block (which of the two is not
  * specified) are skipped and reported as MLA_ERR_SHAPE.
  */

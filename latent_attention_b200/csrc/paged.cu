@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kGatherThreads)
         const int blk = table[(int64_t)b * max_blocks + j / pool.bs];
         if (blk >= 0 && blk < pool.n_blocks) {
           o = ((int64_t)blk * pool.bs + j % pool.bs) * pool.W;
-          s = pool.scales[blk];
+          s = read_scale(pool.scales[blk], &flags);
         } else {
           atomicOr(&flags, kStatusBadPage);
         }

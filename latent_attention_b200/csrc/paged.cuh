@@ -58,6 +58,14 @@ __device__ __forceinline__ bool stored_exp(float scale, int* e) {
   *e = (int)(b >> 23) - 127;
   return (b & 0x807fffffu) == 0 && *e >= kMinExp && *e <= 120;
 }
+// A stored scale to read values with: 1, reported, for one that the append does
+// not write.
+__device__ __forceinline__ float read_scale(float scale, uint32_t* status) {
+  int e;
+  if (stored_exp(scale, &e)) return scale;
+  atomicOr(status, kStatusBadPage);
+  return 1.f;
+}
 
 // 32 bytes at a 32-byte aligned address in one access: a warp's whole sectors,
 // where two accesses of 16 bytes would each touch half of every sector.

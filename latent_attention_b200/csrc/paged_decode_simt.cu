@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(PagedDecodeArgs a
       id = 0;
     }
     blk[g] = id;
-    scl[g] = a.pool.scales[id];
+    scl[g] = read_scale(a.pool.scales[id], a.status);
   }
   for (int c = tid; c < w; c += kThreads) q[c] = Elem<T>::load(ql + c);
   __syncthreads();

@@ -535,11 +535,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
     auto look_up = [&]() {
       if (pending) {
         const int at = (lg - 1) % GR;
-        int e;
-        if (!stored_exp(sc, &e)) {
-          atomicOr(p.status, kStatusBadPage);
-          sc = 1.f;
-        }
+        sc = read_scale(sc, p.status);
         if (lane < 8) sh.scl[at][lane] = sc;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.e_full[at]);

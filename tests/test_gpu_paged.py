@@ -335,6 +335,23 @@ def test_gather_reports_what_is_out_of_range(cuda):
         assert cu[-1] == n_rows
 
 
+BAD_SCALES = [float("nan"), float("inf"), 0.0, -1.0, 3.0, 2.0 ** -65, 2.0 ** 121]
+
+
+@pytest.mark.parametrize("bad", BAD_SCALES)
+def test_gather_reads_a_broken_scale_as_one(cuda, bad):
+    ctx, bs = [40, 20], 16
+    table, n = make_tables(np.random.default_rng(0), ctx, bs, extra_width=0)
+    cache, scales = dirty_pool(n, bs, width(F32), 8)
+    broken, as_one = scales.clone(), scales.clone()
+    broken[table[0, 1]], as_one[table[0, 1]] = bad, 1.0
+    want = np.concatenate([O.rows_of(cache, as_one, table, ctx, b, bs) for b in range(2)])
+    rows, _, ws = run_gather(F32, cache, broken, table, ctx, bs, 60)
+    with pytest.raises(L.MlaError, match="SHAPE"):
+        L.mla_check_device_status(ws)
+    assert np.array_equal(rows[:60], want, equal_nan=True)
+
+
 # ------------------------------------------------------------------ decode
 def decode_inputs(cfg, ctx, bs, seed, spread=2.0, poison=True):
     """Blocks of normalised rows; everything that no token owns (blocks of no
@@ -555,6 +572,25 @@ def test_decode_reports_what_is_out_of_range(cuda, cfg):
             L.mla_check_device_status(ws)
         keep = [0, 2]
         assert oracle.max_rel_err(out[keep], want[keep]) <= TOL[cfg.dtype]
+
+
+@pytest.mark.parametrize("bad", BAD_SCALES)
+@pytest.mark.parametrize("cfg", [F32, bf16(24)], ids=["f32", "h24"])
+def test_decode_reads_a_broken_scale_as_one(cuda, cfg, bad):
+    bs = 16
+    d = decode_inputs(cfg, [100, 50, 64], bs, 8, poison=False)
+    at = int(d["table"][1, 1])
+    g = torch.Generator().manual_seed(9)
+    d["cache"][at] = torch.randn(bs, width(cfg), generator=g).to(FP8).view(torch.uint8)
+    scales = d["scales"].clone()
+    scales[at] = 1.0
+    want = want_decode(cfg, dict(d, scales=scales), bs)
+    scales = scales.clone()
+    scales[at] = bad
+    out, ws = run_decode_paged(cfg, dict(d, scales=scales), bs, check=False)
+    with pytest.raises(L.MlaError, match="SHAPE"):
+        L.mla_check_device_status(ws)
+    assert oracle.max_rel_err(out, want) <= TOL[cfg.dtype]
 
 
 def test_decode_shares_blocks_between_requests(cuda):
