@@ -373,7 +373,8 @@ MLA_API mla_status mla_decode_absorbed(const mla_config* cfg, const void* q_nope
  * row j % block_size of block block_table[b][j / block_size].  Limits:
  * block_size 16, 32, 64 or 128; kv_lora_rank + rope a multiple of 16; at most
  * 8192 requests a call; n_blocks * block_size and max_blocks * block_size
- * below 2^31 (byte offsets are 64-bit).  Integer arrays, scales and tables
+ * below 2^31 (byte offsets are 64-bit); n_rows in [1, 2^30], capacities in
+ * [0, 2^30].  Integer arrays, scales and tables
  * need 4-byte alignment, cache and rows 16, workspaces 256.
  *
  * Lengths, block ids, slots and scales are read on the device only.  One that
@@ -496,6 +497,10 @@ MLA_API size_t mla_decode_paged_workspace_size(const mla_config* cfg, int32_t B,
  *   block_table  [B, max_blocks];  ctx_len [B], counting the current token; a
  *                request without tokens (ctx_len 0) gets a zero row
  * Rows of a block behind the last token are never used, whatever they hold.
+ * Requests may share blocks (the plan gives every block to one request; who
+ * shares them keeps the count).  On tensor cores latent values must stay below
+ * 2^80 in magnitude: weights up to 2^24 relative to a segment's first token
+ * multiply them in fp32.
  */
 MLA_API mla_status mla_decode_paged(const mla_config* cfg, const void* q_nope, const void* q_pe,
                                     const void* w_kv_b, const void* cache, const float* scales,

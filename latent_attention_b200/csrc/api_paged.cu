@@ -14,6 +14,9 @@ using mla::cuda_fail;
 using mla::fail;
 using mla::kMaxRequests;
 
+// Most rows or slots of a call: row counts rounded up to whole grids stay ints.
+constexpr int32_t kMaxRows = 1 << 30;
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // n_blocks and block_size of a pool.
@@ -145,7 +148,8 @@ mla_status mla_paged_plan(const int32_t* ctx_len, const int32_t* new_len, int32_
   mla_status s = check_pool(n_blocks, block_size);
   if (s == MLA_OK) s = check_table(B, max_blocks, block_size);
   if (s != MLA_OK) return s;
-  if (capacity < 0) return fail(MLA_ERR_SHAPE, "capacity=%d", capacity);
+  if (capacity < 0 || capacity > kMaxRows)
+    return fail(MLA_ERR_SHAPE, "capacity=%d outside [0, 2^30]", capacity);
   const void* ptrs[] = {ctx_len, new_len, block_table, free_ring, free_state, ctx_out,
                         free_state_out, slot_map, positions, cu_new};
   for (const void* p : ptrs)
@@ -171,7 +175,8 @@ mla_status mla_paged_append(const mla_config* cfg, const void* rows, const int32
   s = check_pool(n_blocks, block_size);
   if (s == MLA_OK) s = check_row(*cfg);
   if (s != MLA_OK) return s;
-  if (n_rows < 1) return fail(MLA_ERR_SHAPE, "n_rows=%d", n_rows);
+  if (n_rows < 1 || n_rows > kMaxRows)
+    return fail(MLA_ERR_SHAPE, "n_rows=%d outside [1, 2^30]", n_rows);
   if (!aligned16(rows) || !aligned16(cache))
     return fail(MLA_ERR_ALIGN, "rows or cache is not 16-byte aligned");
   if (!aligned4(slot_map) || !aligned4(scales))
@@ -206,7 +211,8 @@ mla_status mla_paged_gather(const mla_config* cfg, const void* cache, const floa
   if (s == MLA_OK) s = check_table(B, max_blocks, block_size);
   if (s == MLA_OK) s = check_row(*cfg);
   if (s != MLA_OK) return s;
-  if (capacity < 0) return fail(MLA_ERR_SHAPE, "capacity=%d", capacity);
+  if (capacity < 0 || capacity > kMaxRows)
+    return fail(MLA_ERR_SHAPE, "capacity=%d outside [0, 2^30]", capacity);
   if (!aligned16(cache) || !aligned16(rows_out))
     return fail(MLA_ERR_ALIGN, "cache or rows_out is not 16-byte aligned");
   if (!aligned4(scales) || !aligned4(block_table) || !aligned4(ctx_len) || !aligned4(cu_ctx))

@@ -443,6 +443,21 @@ def test_decode_bf16_many_requests(cuda, heads):
     check_decode(bf16(heads), ctx, 32, seed=heads)
 
 
+@pytest.mark.parametrize("cfg", [F32, bf16(16), bf16(65)], ids=["f32", "h16", "h65"])
+def test_decode_of_the_most_requests(cuda, cfg):
+    rng = np.random.default_rng(3)
+    B, bs = 8192, 16
+    ctx = [int(x) for x in rng.integers(0, 41, B)]
+    d = decode_inputs(cfg, ctx, bs, 3)
+    out, _ = run_decode_paged(cfg, d, bs)
+    some = sorted(set(rng.integers(0, B, 60).tolist()) | {0, 31, 32, 127, 128, B - 1})
+    part = dict(d, q_nope=d["q_nope"][some], q_pe=d["q_pe"][some], table=d["table"][some],
+                ctx=[ctx[b] for b in some])
+    assert oracle.max_rel_err(out[some], want_decode(cfg, part, bs)) <= TOL[cfg.dtype]
+    for b, n in enumerate(ctx):
+        assert n or (out[b] == 0).all()
+
+
 def test_decode_bf16_other_widths_run_on_cuda_cores(cuda):
     cfg = bf16(3, kv_lora_rank=96, qk_rope_head_dim=32, qk_nope_head_dim=24, v_head_dim=40)
     check_decode(cfg, [0, 1, 1500, 64], 32, seed=9)

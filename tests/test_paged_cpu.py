@@ -91,7 +91,8 @@ def plan_args(**kw):
     (dict(ctx=_p(0)), 1), (dict(slots=_p(0)), 1), (dict(ws=_p(0)), 1), (dict(cu=_p(0)), 1),
     (dict(bs=48), 2), (dict(bs=0), 2), (dict(B=0), 2), (dict(B=8193), 2),
     (dict(max_blocks=0), 2), (dict(max_blocks=1 << 28), 2), (dict(n_blocks=0), 2),
-    (dict(n_blocks=1 << 27), 2), (dict(capacity=-1), 2), (dict(table=_p(A + 2)), 3),
+    (dict(n_blocks=1 << 27), 2), (dict(capacity=-1), 2), (dict(capacity=(1 << 30) + 1), 2),
+    (dict(capacity=(1 << 31) - 1), 2), (dict(table=_p(A + 2)), 3),
     (dict(ws=_p(A + 16)), 3), (dict(ws_bytes=C.c_size_t(255)), 5)])
 def test_plan_refuses(lib, kw, status):
     assert lib.mla_paged_plan(*plan_args(**kw)) == status
@@ -107,6 +108,7 @@ def append_args(config=BF16, **kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(cfg=None), 1), (dict(rows=_p(0)), 1), (dict(scales=_p(0)), 1), (dict(n=0), 2),
+    (dict(n=(1 << 30) + 1), 2), (dict(n=(1 << 31) - 1), 2),
     (dict(bs=20), 2), (dict(n_blocks=-1), 2), (dict(rows=_p(A + 8)), 3),
     (dict(cache=_p(A + 4)), 3), (dict(slots=_p(A + 1)), 3), (dict(ws=_p(A + 128)), 3),
     (dict(ws_bytes=C.c_size_t(256)), 5)])
@@ -134,6 +136,7 @@ def gather_args(config=BF16, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(cache=_p(0)), 1), (dict(rows=_p(0)), 1), (dict(cu=_p(0)), 1), (dict(B=-1), 2),
     (dict(max_blocks=0), 2), (dict(bs=17), 2), (dict(capacity=-2), 2), (dict(rows=_p(A + 2)), 3),
+    (dict(capacity=(1 << 30) + 1), 2), (dict(capacity=(1 << 31) - 1), 2),
     (dict(ctx=_p(A + 2)), 3), (dict(ws_bytes=C.c_size_t(0)), 5)])
 def test_gather_refuses(lib, kw, status):
     assert lib.mla_paged_gather(*gather_args(**kw)) == status
