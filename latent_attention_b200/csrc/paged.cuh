@@ -38,6 +38,19 @@ __device__ __forceinline__ void from_e4m3x4(uint32_t v, float (&f)[4]) {
   }
 }
 
+// (d0, d1) *= (a0, a1) in one packed instruction.
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1) {
+  asm("{\n\t.reg .b64 a, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 d, {%0, %1};\n\t"
+      "mul.rn.f32x2 d, d, a;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // 2^e for e in [-126, 127]; 0 below, 2^127 above.
 __device__ __forceinline__ float pow2(int e) {
   return e < -126 ? 0.f : __int_as_float((min(e, 127) + 127) << 23);

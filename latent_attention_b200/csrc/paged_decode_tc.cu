@@ -194,18 +194,6 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t* r) {
   static_assert(N == 8 || N == 16, "columns");
   if (N == 8) tmem_ld8(taddr, r); else tmem_ld16(taddr, r);
 }
-// (d0, d1) *= (a0, a1) in one packed instruction.
-__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1) {
-  asm("{\n\t.reg .b64 a, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 d, {%0, %1};\n\t"
-      "mul.rn.f32x2 d, d, a;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "+f"(d0), "+f"(d1)
-      : "f"(a0), "f"(a1));
-}
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
