@@ -14,10 +14,12 @@
 // The query's product is warp-level MMAs, whose results the threads round where
 // they hold them, a row of q_lat in one warp's quads; the output's is tcgen05
 // with the 128 columns as M and the sequences as N (as warp-level MMAs, some 19
-// cycles each, it took 5000 cycles of 12500 for 16 sequences).  (Four blocks a head, in a cluster, took longer: 45 us
-// against 26 at 64 sequences of 128 heads.)  Neither q_lat nor o_lat is rounded
-// to 16 bits: q_lat goes from fp32 to its two terms, o_lat enters the product as
-// two bf16 terms (16 significant bits).
+// cycles each, it took 5000 cycles of 12500 for 16 sequences).  (Four blocks a
+// head, in a cluster, took longer: 45 us against 26 for both kernels at 64
+// sequences of 128 heads.)  Neither q_lat nor o_lat is rounded to 16 bits: q_lat
+// goes from fp32 to its two terms, o_lat enters the product as two bf16 terms (16
+// significant bits).  A whole call of 4 sequences and 128 heads takes 24.7 us, of
+// which the two kernels take some 6 each: the 33 MB of weights would take 5.
 #include <algorithm>
 
 #include "paged.cuh"
