@@ -97,21 +97,6 @@ __device__ __forceinline__ bool aligned32(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
 }
 
-// 16 consecutive elements as floats (16-byte aligned source).
-__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 x = reinterpret_cast<const float4*>(p)[i];
-    v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
-  }
-}
-__device__ __forceinline__ void store16(float* p, const float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    reinterpret_cast<float4*>(p)[i] =
-        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-}
-
 // 16 elements of a row as they lie in memory, 32 or 64 bytes.  wide: the
 // address is 32-byte aligned.
 template <typename T> struct Piece;

@@ -132,7 +132,6 @@ struct AttnParams {
   const int32_t* len;          // [B] tokens
   const int4* first;           // [n_units][2] a unit's first segment: b, c0, nch, slot; whole, tokens
   const int32_t* table;        // [B, max_blocks]
-  const uint8_t* cache;
   const float* scales;
   const float* qf;             // [B, groups, NH]
   int B, max_blocks, n_blocks, bs, lbs;
@@ -905,7 +904,7 @@ cudaError_t tc_paged_decode(const PagedDecodeArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
   AttnParams p{};
   p.pre = a.pre; p.len = a.len; p.first = (const int4*)a.first; p.table = a.table;
-  p.cache = a.pool.cache; p.scales = a.pool.scales; p.qf = a.qf;
+  p.scales = a.pool.scales; p.qf = a.qf;
   p.B = a.B; p.max_blocks = a.max_blocks; p.n_blocks = a.pool.n_blocks; p.bs = a.pool.bs;
   p.lbs = a.pool.bs == 16 ? 4 : a.pool.bs == 32 ? 5 : a.pool.bs == 64 ? 6 : 7;
   p.h = a.h; p.groups = t.groups; p.hg_heads = t.hg_heads;

@@ -1,5 +1,5 @@
 // How the tensor-core paged decode divides its work.  Host and device code,
-// shared by the attention kernel, the combine kernel and a host-side check.
+// shared by the attention kernel, those around it and a host-side check.
 //
 // A sequence of n > 0 tokens is ceil(n / CT) chunks of CT tokens, and starting
 // it is charged kSeqCost chunks.  pre[b] is the number of charged chunks of
@@ -8,7 +8,7 @@
 // unit's segment of b is the part of b's chunks in its slice.  A segment that
 // holds all of b is written to the output directly; any other leaves a partial
 // result in slot 2u (the sequence began in an earlier slice) or 2u + 1 (it
-// begins here and goes on), which the combine kernel merges.
+// begins here and goes on), which the output kernel merges.
 #pragma once
 #include <cstdint>
 

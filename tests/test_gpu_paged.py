@@ -436,6 +436,12 @@ def test_decode_bf16_long_and_mixed(cuda, bs):
     check_decode(bf16(16), [30011], bs, seed=bs + 1, with_o=True)
 
 
+@pytest.mark.parametrize("heads,chunks", [(16, 12), (128, 6)])
+def test_decode_bf16_requests_of_one_to_many_partials(cuda, heads, chunks):
+    # slices of some `chunks` chunks: request k is cut into about k pieces
+    check_decode(bf16(heads), [128 * chunks * k + 5 for k in range(13)] + [1], 64, seed=heads)
+
+
 @pytest.mark.parametrize("heads", [16, 128])
 def test_decode_bf16_many_requests(cuda, heads):
     rng = np.random.default_rng(heads)
