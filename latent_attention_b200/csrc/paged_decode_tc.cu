@@ -778,11 +778,13 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
           st_shared_v2(pt + lo_tile + swz<K::PW>(at + lo_at), lb[0], lb[1]);
         }
         // a weight of 0 times whatever lies behind the last token could be NaN
+        // (neighbouring rows take their pieces in another order: one bank's
+        // would make it 2 us for a chunk of a few tokens)
         if (!live) {
           for (int i = grp; i < 32; i += NG) {
             const int slot = (4 * g + (i >> 3)) % NS;
-            st_shared_v4(smem_u32(smem + K::OFF_C + slot * BOX) + row * 128 + (i & 7) * 16, 0, 0, 0,
-                         0);
+            st_shared_v4(smem_u32(smem + K::OFF_C + slot * BOX) + row * 128 +
+                             (((i + lane) & 7) << 4), 0, 0, 0, 0);
           }
         }
         fence_proxy_async();

@@ -23,18 +23,23 @@ using namespace sm100;
 constexpr int NT = 128;
 constexpr int ABOX = 128 * 128;          // 128 weight rows x 64 of K, bf16
 constexpr int BN = 128;                  // sequences a block, at most
-constexpr int STAGES = 4;
+constexpr int MAX_STAGES = 10;           // 64 of K each, in 200 KB
 
 struct OprojParams {
   __nv_bfloat16* out;                    // [B, hidden]
   int B, hidden, chunks;                 // K / 64, rounded up
   int bn;                                // sequences a block, multiple of 16
+  int stages;
   uint32_t* status;
 };
 __host__ __device__ constexpr int stage_bytes(int bn) { return ABOX + 2 * bn * 128; }
+// As deep a ring as fits: what streams is the weights, and four stages of them
+// are too few in flight (16 sequences, 235 MB of weights: 64 us between events for
+// 56; 4 sequences, 67 MB: 25.4 for 23.3).
+int stages_of(int bn) { return std::min(MAX_STAGES, 200 * 1024 / stage_bytes(bn)); }
 int smem_of(int bn) {
   // the ring, later the block's sums [bn][132]
-  return std::max(STAGES * stage_bytes(bn), bn * 132 * 4) + 1024;
+  return std::max(stages_of(bn) * stage_bytes(bn), bn * 132 * 4) + 1024;
 }
 
 template <bool USE>
@@ -61,7 +66,7 @@ __global__ void __launch_bounds__(NT) paged_oproj_kernel(const __grid_constant__
                                                          const __grid_constant__ CUtensorMap tmL,
                                                          OprojParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[STAGES], empty[STAGES], done;
+  __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], done;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -73,7 +78,7 @@ __global__ void __launch_bounds__(NT) paged_oproj_kernel(const __grid_constant__
   const int c1 = (int)((int64_t)p.chunks * (piece + 1) / n_pieces);
   const uint32_t cols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : 128;
   if (t == 0) {
-    for (int i = 0; i < STAGES; ++i) {
+    for (int i = 0; i < MAX_STAGES; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -91,42 +96,47 @@ __global__ void __launch_bounds__(NT) paged_oproj_kernel(const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = tmem_base;
-  const int stage = stage_bytes(p.bn);
-  auto load_w = [&](int i) {
-    uint8_t* at = smem + (i % STAGES) * stage;
-    mbar_arrive_expect_tx(&full[i % STAGES], stage);
-    tma_load_2d(at, &tmW, (c0 + i) * 64, n0, &full[i % STAGES]);
+  const int stage = stage_bytes(p.bn), stages = p.stages;
+  // chunk i of the piece into slot s
+  auto load_w = [&](int i, int s) {
+    mbar_arrive_expect_tx(&full[s], stage);
+    tma_load_2d(smem + s * stage, &tmW, (c0 + i) * 64, n0, &full[s]);
   };
-  auto load_o = [&](int i) {
-    uint8_t* at = smem + (i % STAGES) * stage;
-    tma_load_2d(at + ABOX, &tmO, (c0 + i) * 64, b0, &full[i % STAGES]);
-    tma_load_2d(at + ABOX + p.bn * 128, &tmL, (c0 + i) * 64, b0, &full[i % STAGES]);
+  auto load_o = [&](int i, int s) {
+    uint8_t* at = smem + s * stage + ABOX;
+    tma_load_2d(at, &tmO, (c0 + i) * 64, b0, &full[s]);
+    tma_load_2d(at + p.bn * 128, &tmL, (c0 + i) * 64, b0, &full[s]);
   };
   const int n = c1 - c0;
   volatile int* abort_v = &abort_flag;
   // the first weights do not depend on the kernel before this one (which
   // started only once all before it had finished)
   if (t == 32)
-    for (int i = 0; i < min(n, STAGES); ++i) load_w(i);
+    for (int i = 0; i < min(n, stages); ++i) load_w(i, i);
   griddep_wait();
   griddep_launch_dependents();
   if (warp == 1) {
     if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 1;
       for (int i = 0; i < n; ++i) {
-        if (i >= STAGES) {
-          if (!mbar_wait(&empty[i % STAGES], (i / STAGES - 1) & 1, abort_v, p.status)) break;
-          load_w(i);
+        if (i >= stages) {
+          if (!mbar_wait(&empty[s], ph, abort_v, p.status)) break;
+          load_w(i, s);
         }
-        load_o(i);
+        load_o(i, s);
+        if (++s == stages) { s = 0; ph ^= 1; }
       }
     }
   } else if (warp == 2) {
     if (elect_one()) {
       const uint32_t base = smem_u32(smem), idesc = idesc_bf16(128, p.bn);
+      int s = 0;
+      uint32_t ph = 0;
       for (int i = 0; i < n; ++i) {
-        if (!mbar_wait(&full[i % STAGES], (i / STAGES) & 1, abort_v, p.status)) break;
+        if (!mbar_wait(&full[s], ph, abort_v, p.status)) break;
         tc_fence_after();
-        const uint32_t at = base + (i % STAGES) * stage;
+        const uint32_t at = base + s * stage;
         const uint64_t da = desc_kmajor_sw128(at), dh = desc_kmajor_sw128(at + ABOX);
         const uint64_t dl = desc_kmajor_sw128(at + ABOX + p.bn * 128);
 #pragma unroll
@@ -134,7 +144,8 @@ __global__ void __launch_bounds__(NT) paged_oproj_kernel(const __grid_constant__
           mma_keep<false>(tbase, da + 2 * k, dh + 2 * k, idesc, (i | k) != 0);
           mma_keep<true>(tbase, da + 2 * k, dl + 2 * k, idesc, 1);
         }
-        mma_commit(&empty[i % STAGES]);
+        mma_commit(&empty[s]);
+        if (++s == stages) { s = 0; ph ^= 1; }
       }
       mma_commit(&done);
     }
@@ -198,6 +209,7 @@ cudaError_t launch_paged_oproj(const void* o, const void* o_lo, const void* w_o,
   p.hidden = hidden;
   p.chunks = (K + 63) / 64;
   p.bn = std::min(BN, (B + 15) / 16 * 16);
+  p.stages = stages_of(p.bn);
   p.status = status;
   const int tiles = (hidden + 127) / 128, rows = (B + p.bn - 1) / p.bn;
   // pieces of K: blocks for every SM, eight chunks a piece at least
@@ -211,7 +223,7 @@ cudaError_t launch_paged_oproj(const void* o, const void* o_lo, const void* w_o,
       !encode_tmap(&tmL, o_lo, 2, od, str, ob))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> set{0};
-  const cudaError_t e = set_dynamic_smem((const void*)paged_oproj_kernel, smem_of(BN), set);
+  const cudaError_t e = set_dynamic_smem((const void*)paged_oproj_kernel, 201 * 1024, set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles, pieces, rows);

@@ -180,8 +180,9 @@ __device__ __forceinline__ uint2 quad_transpose(const uint32_t (&v)[4], int lane
   return up ? make_uint2(w1, w0) : make_uint2(w0, w1);
 }
 
-// Block (x, y): x = 0 the lengths, 1 .. h a head, h + 1 the rows that pad the
-// head groups; y: 32 x rounds sequences
+// Block (x, y): x = 0 the lengths, 1 .. h a head, from h + 1 on a row that pads
+// the head groups (a block each: one block for 15 of them took 12 us longer); y:
+// 32 x rounds sequences
 __global__ void __launch_bounds__(NT) paged_query_kernel(const __grid_constant__ CUtensorMap tmW,
                                                          QueryParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -207,18 +208,16 @@ __global__ void __launch_bounds__(NT) paged_query_kernel(const __grid_constant__
     return;
   }
   if ((int)blockIdx.x > p.h) {
-    const int pad = p.groups * p.NH - p.h;
-    for (int k = t; k < nb * pad * 2 * (W / 16); k += NT) {
-      const int c = k % (W / 16), term = k / (W / 16) % 2, j = k / (W / 8) % pad;
-      const int64_t b = b0 + k / (W / 8) / pad;
-      // pad row j: groups are full but for the last rows of each
-      int g = 0, i = j;
-      for (; g < p.groups; ++g) {
-        const int real = min(p.hg_heads, p.h - g * p.hg_heads), n = p.NH - real;
-        if (i < n) { i += real; break; }
-        i -= n;
-      }
-      const int64_t bg = b * p.groups + g;
+    // pad row j: groups are full but for the last rows of each
+    int g = 0, i = (int)blockIdx.x - p.h - 1;
+    for (; g < p.groups; ++g) {
+      const int real = min(p.hg_heads, p.h - g * p.hg_heads), n = p.NH - real;
+      if (i < n) { i += real; break; }
+      i -= n;
+    }
+    for (int k = t; k < nb * 2 * (W / 16); k += NT) {
+      const int c = k % (W / 16), term = k / (W / 16) % 2;
+      const int64_t bg = (int64_t)(b0 + k / (W / 8)) * p.groups + g;
       *reinterpret_cast<uint4*>(p.q8 + ((bg * 2 + term) * p.NH + i) * W + c * 16) =
           make_uint4(0u, 0u, 0u, 0u);
       if (c == 0 && term == 0) p.qf[bg * p.NH + i] = 0.f;
@@ -641,11 +640,10 @@ cudaError_t launch_paged_query(const PagedDecodeArgs& a, int min_len, cudaStream
   q.scale_log2 = a.scale * 1.4426950408889634f;
   q.status = a.status;
   q.rounds = rounds_of(a);
-  const bool pads = q.groups * q.NH > q.h;
+  const int pads = q.groups * q.NH - q.h;
   count_launches();
-  return launch_pdl(paged_query_kernel, dim3(1 + a.h + pads, (a.B + MB * q.rounds - 1) / (MB * q.rounds)), dim3(NT),
-                    Q_SMEM,
-                    st, tmW, q);
+  const dim3 grid(1 + a.h + pads, (a.B + MB * q.rounds - 1) / (MB * q.rounds));
+  return launch_pdl(paged_query_kernel, grid, dim3(NT), Q_SMEM, st, tmW, q);
 }
 
 cudaError_t launch_paged_output(const PagedDecodeArgs& a, cudaStream_t st) {
