@@ -255,8 +255,10 @@ cudaError_t launch_latent_finalize(int dtype, const void* ckv,
 cudaError_t launch_decode_simt(int dtype, const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st);
 // Rows up to which an append finds a block's second run by looking through the
-// slots before it; beyond, a bit per block (claims, zeroed with the status)
-// tells.
+// slots before it; beyond, a bit per block (claims, zeroed with the status by a
+// memset of its own) tells.  Around 4000 rows in runs of 64 the look takes 5.5 us
+// for 8.3 with the bits, in runs of one 12.4 for 10.9; around 8000, 8.2 for 10.4
+// and (6000) 21.4 for 16.4.
 constexpr int kAppendScan = 4096;
 cudaError_t launch_paged_append(int dtype, const void* rows, const int32_t* slots, int n_rows,
                                 const PagedPool& pool, uint32_t* status, uint32_t* claims,

@@ -222,7 +222,9 @@ __device__ __forceinline__ void report(uint32_t* status, uint32_t flags, bool ow
   }
 }
 
-constexpr int kShortRun = 4;
+// (500 runs of 6 rows: 9.1 us, 14.9 with the limit at 4; at 16, 195 runs of 26
+// rows, cut by blocks of 64, take 14.5 us for 12.5.)
+constexpr int kShortRun = 8;
 
 // Largest |x| of a piece as bits, NaN and infinity above all numbers.
 __device__ __forceinline__ uint32_t largest(const Piece<float>& x) {
@@ -272,11 +274,13 @@ __device__ __forceinline__ void append_run(const T* __restrict__ rows,
     if (t + q * G < nv) load_piece(src + (t + q * G) * 16, wide, held[q]);
   // two runs of one call in one block have no order: the second is refused
   uint32_t refused = 0;
-  if (claims) {
+  if (G == 256 || claims) {                  // (256 threads: many rows, always by claims)
     const uint32_t bit = 1u << (blk & 31);
     if (t == 0 && (atomicOr(&claims[blk >> 5], bit) & bit)) refused = 1;
   } else {
-    for (int q = t; q < i; q += G) refused |= slots[q] >= 0 && slots[q] / bs == blk;
+    const int lbs = __ffs(bs) - 1;           // (a negative slot stays negative)
+#pragma unroll 8
+    for (int q = t; q < i; q += G) refused |= slots[q] >> lbs == blk;
   }
   const float old_scale = off > 0 ? pool.scales[blk] : 1.f;
   uint32_t amax = 0, odd = 0;
@@ -388,13 +392,13 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : sizeof(T) == 4 ? 4 : 3)
   if constexpr (NT == 1024) {
     for (int k = t / 32; apart && k < todo; k += NT / 32)
       if (lens[k] <= kShortRun)
-        append_run<T, 32, sizeof(T) == 2 ? 5 : 2>(rows, slots, pool, starts[k], sl[starts[k] - w0 + 1], lens[k], t & 31,
-                             wide, claims, &flags,
-                             [](uint32_t& amax, uint32_t& odd, uint32_t& refused) {
-                               amax = __reduce_max_sync(0xffffffffu, amax);
-                               odd = __reduce_or_sync(0xffffffffu, odd);
-                               refused = __reduce_or_sync(0xffffffffu, refused);
-                             });
+        append_run<T, 32, sizeof(T) == 2 ? 4 : 2>(
+            rows, slots, pool, starts[k], sl[starts[k] - w0 + 1], lens[k], t & 31, wide, claims,
+            &flags, [](uint32_t& amax, uint32_t& odd, uint32_t& refused) {
+              amax = __reduce_max_sync(0xffffffffu, amax);
+              odd = __reduce_or_sync(0xffffffffu, odd);
+              refused = __reduce_or_sync(0xffffffffu, refused);
+            });
   }
   for (int k = 0; k < todo; ++k) {
     if (apart && lens[k] <= kShortRun) continue;
@@ -425,7 +429,7 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : sizeof(T) == 4 ? 4 : 3)
                             });
   }
   __syncthreads();
-  report(status, flags, !claims);
+  report(status, flags, NT == 1024 && !claims);
 }
 
 // ----------------------------------------------------------------- gather
@@ -566,7 +570,8 @@ cudaError_t launch_paged_append(int dtype, const void* rows, const int32_t* slot
   const int windows = few ? 148 : 4 * 148;
   const int window = std::min((n_rows + windows - 1) / windows, pool.bs);
   const int grid = (n_rows + window - 1) / window;
-  if (n_rows <= kAppendScan) claims = nullptr;   // (at most 592 blocks)
+  static_assert(kAppendScan < 2 * 148 * 16, "256-thread blocks take claims");
+  if (n_rows <= kAppendScan) claims = nullptr;   // (at most 4096 / 16 blocks)
   count_launches();
   const auto go = [&](auto kernel, auto* p, int nt) {
     kernel<<<grid, nt, 0, st>>>(p, slots, n_rows, pool, window, status, claims);
