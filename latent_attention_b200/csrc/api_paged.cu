@@ -17,6 +17,12 @@ using mla::kMaxRequests;
 // Most rows or slots of a call: row counts rounded up to whole grids stay ints.
 constexpr int32_t kMaxRows = 1 << 30;
 
+// fp32 output projection: up to this many rows a warp per output column, beyond
+// the tiles of the prefill.  Whole calls of 16 heads and 2048 columns: 8 rows 20
+// us for 59, 64 rows 41 for 69, 128 rows 77 for 80; of 4 heads and 256 columns: 8
+// rows 14 for 25, 128 rows 19 for 31.
+constexpr int kSkinnyRows = 128;
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // n_blocks and block_size of a pool.
@@ -302,6 +308,9 @@ mla_status mla_decode_paged(const mla_config* cfg, const void* q_nope, const voi
   if (w_o) {
     if (tc) {
       e = mla::launch_paged_oproj(a.o, a.o_lo, w_o, out, B, a.h * a.dv, c.hidden_size, a.status, st);
+    } else if (c.dtype == MLA_F32 && B <= kSkinnyRows) {
+      e = mla::launch_paged_oproj_simt((const float*)a.o, (const float*)w_o, (float*)out, B,
+                                       a.h * a.dv, c.hidden_size, st);
     } else {
       mla::GemmArgs go;
       go.A = a.o; go.lda = (int64_t)a.h * a.dv; go.M = B; go.K = a.h * a.dv; go.nseg = 1;

@@ -272,6 +272,8 @@ constexpr int kMaxSmem = 227 * 1024 - 1024;
 inline int paged_simt_smem(int w, int split_tokens) {
   return 4 * (w + 1024 + split_tokens + 2 * (split_tokens / 16));
 }
+cudaError_t launch_paged_oproj_simt(const float* o, const float* w_o, float* out, int B, int K,
+                                    int hidden, cudaStream_t st);
 cudaError_t launch_paged_decode_simt(int dtype, const PagedDecodeArgs& a, cudaStream_t st);
 // Smallest workspace mla_decode_absorbed runs with (one SM pair on tensor cores).
 size_t decode_min_workspace(const mla_config& c, int B, int max_ctx);

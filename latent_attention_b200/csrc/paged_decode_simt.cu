@@ -230,6 +230,37 @@ __global__ void __launch_bounds__(kThreads) paged_merge_kernel(PagedDecodeArgs a
   }
 }
 
+// out = o W_o^T for a few rows, fp32: a warp per column of the output and up to
+// ROWS sequences, the lanes sharing K.
+constexpr int ROWS = 8;
+
+__global__ void __launch_bounds__(kThreads)
+    paged_oproj_simt_kernel(const float* __restrict__ o, const float* __restrict__ w_o,
+                            float* __restrict__ out, int B, int K, int hidden) {
+  sm100::griddep_wait();
+  sm100::griddep_launch_dependents();
+  const int col = blockIdx.x * (kThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int b0 = blockIdx.y * ROWS, n = min(ROWS, B - b0);
+  if (col >= hidden) return;
+  const float* w = w_o + (int64_t)col * K;
+  const float* x = o + (int64_t)b0 * K;
+  float acc[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) acc[r] = 0.f;
+#pragma unroll 2
+  for (int k = lane; k < K; k += 32) {
+    const float v = w[k];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+      if (r < n) acc[r] = fmaf(v, x[(int64_t)r * K + k], acc[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    for (int s = 16; s; s >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], s);
+    if (lane == 0 && r < n) out[(int64_t)(b0 + r) * hidden + col] = acc[r];
+  }
+}
+
 template <typename T>
 cudaError_t run(const PagedDecodeArgs& a, cudaStream_t st) {
   const dim3 bh(a.B, a.h);
@@ -256,6 +287,13 @@ cudaError_t run(const PagedDecodeArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t launch_paged_oproj_simt(const float* o, const float* w_o, float* out, int B, int K,
+                                    int hidden, cudaStream_t st) {
+  const dim3 grid((hidden + kThreads / 32 - 1) / (kThreads / 32), (B + ROWS - 1) / ROWS);
+  count_launches();
+  return launch_pdl(paged_oproj_simt_kernel, grid, dim3(kThreads), 0, st, o, w_o, out, B, K, hidden);
+}
 
 cudaError_t launch_paged_decode_simt(int dtype, const PagedDecodeArgs& a, cudaStream_t st) {
   return dtype == MLA_F32 ? run<float>(a, st) : run<__nv_bfloat16>(a, st);

@@ -423,6 +423,12 @@ def test_decode_f32(cuda, bs, ctx, with_o):
     check_decode(F32, ctx, bs, seed=len(ctx), with_o=with_o)
 
 
+@pytest.mark.parametrize("B", [1, 7, 8, 9, 128, 129])
+def test_decode_f32_output_projection_rows(cuda, B):
+    check_decode(F32.with_(hidden_size=40), [(3 * b) % 50 for b in range(B)], 16, seed=B,
+                 with_o=True)
+
+
 @pytest.mark.parametrize("heads", [1, 5, 16, 31, 48, 64, 96, 128])
 @pytest.mark.parametrize("bs,ctx", [
     (16, [1, 17, 0, 500]), (64, [127, 128, 129, 64, 1]), (128, [700, 1, 0, 1300])])
