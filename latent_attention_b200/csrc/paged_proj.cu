@@ -18,7 +18,7 @@
 // head, in a cluster, took longer: 45 us against 26 for both kernels at 64
 // sequences of 128 heads.)  Neither q_lat nor o_lat is rounded to 16 bits: q_lat
 // goes from fp32 to its two terms, o_lat enters the product as two bf16 terms (16
-// significant bits).  A whole call of 4 sequences and 128 heads takes 24.7 us, of
+// significant bits).  A whole call of 4 sequences and 128 heads takes 23.1 us, of
 // which the two kernels take some 6 each: the 33 MB of weights would take 5.
 #include <algorithm>
 
