@@ -941,3 +941,35 @@ def test_decode_other_widths_with_output_projection(cuda):
     cfg = bf16(3, kv_lora_rank=96, qk_rope_head_dim=32, qk_nope_head_dim=24, v_head_dim=40,
                hidden_size=120)
     check_decode(cfg, [0, 70, 300], 32, seed=9, with_o=True)
+
+
+@pytest.mark.parametrize("cfg", [F32, bf16(16)], ids=["f32", "h16"])
+def test_two_captured_graphs_share_a_workspace(cuda, cfg):
+    bs = 16
+    ds = [decode_inputs(cfg, ctx, bs, i) for i, ctx in enumerate(([700, 3, 0], [90] * 40))]
+    dev = [{k: v.cuda() for k, v in d.items() if torch.is_tensor(v)} for d in ds]
+    dt = torch.bfloat16 if cfg.dtype == "bf16" else torch.float32
+    size = max(L.mla_decode_paged_workspace_size(cfg, len(d["ctx"]), d["table"].shape[1], bs)[0]
+               for d in ds)
+    ws = torch.full((size,), 0xff, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for d, g in zip(ds, dev):
+        B, tb, cx = len(d["ctx"]), i32(d["table"]), i32(d["ctx"])
+        out = torch.zeros(B, cfg.num_heads * cfg.v_head_dim, dtype=dt, device="cuda")
+        call = lambda: L.mla_decode_paged(cfg, g["q_nope"], g["q_pe"], g["w"], g["cache"],
+                                          g["scales"], tb, cx, B, tb.shape[1], d["n_blocks"], bs,
+                                          None, out, ws)
+        call()
+        torch.cuda.synchronize()
+        want = out.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        graphs.append((graph, tb, cx))
+        outs.append((out, want))
+    for i in (0, 1, 1, 0, 1, 0):
+        outs[i][0].zero_()
+        graphs[i][0].replay()
+        torch.cuda.synchronize()
+        L.mla_check_device_status(ws)
+        assert torch.equal(outs[i][0], outs[i][1])
