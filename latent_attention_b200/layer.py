@@ -113,6 +113,8 @@ class MlaPagedCache:
         n, self.layout = mla_decode_paged_workspace_size(self.c, max_requests, max_blocks,
                                                          block_size)
         self.decode_ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        for ws in (self.ws, self.decode_ws):
+            ws[:256].zero_()           # MLA_OK until a call leaves its own status
 
     def plan(self, new_len, stream=None):
         """Blocks and slots of ``new_len`` [B] tokens (int32; -1: the request
