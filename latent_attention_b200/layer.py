@@ -7,7 +7,7 @@ their own.
 """
 import torch
 
-from . import (make_config, mla_build_rope_tables, mla_prefill_workspace_size,
+from . import (MlaError, make_config, mla_build_rope_tables, mla_prefill_workspace_size,
                mla_prefill_forward, mla_decode_workspace_size,
                mla_decode_absorbed, mla_check_device_status,
                mla_paged_workspace_size, mla_paged_plan, mla_paged_append,
@@ -86,7 +86,9 @@ class MlaPagedCache:
     the lengths, all on the device.  One serving step is ``plan`` (blocks and
     slots of the new tokens), ``append`` (their latent rows) and ``decode`` or
     ``gather``; nothing in it waits for the device, so a step can be captured
-    into a CUDA graph."""
+    into a CUDA graph.  Each of the four has a workspace of its own, because a
+    call starts its workspace's status afresh: what a plan reported is still
+    there when ``check_status`` reads it at the step's end."""
 
     def __init__(self, cfg, max_requests, max_blocks, n_blocks, block_size=64, capacity=None,
                  device="cuda"):
@@ -108,12 +110,13 @@ class MlaPagedCache:
         self.slots = torch.empty(self.capacity, **i32)
         self.positions = torch.empty(self.capacity, **i32)
         self.cu_new = torch.empty(max_requests + 1, **i32)
-        self.ws = torch.empty(mla_paged_workspace_size(n_blocks), dtype=torch.uint8,
-                              device=self.device)
+        n = mla_paged_workspace_size(n_blocks)
+        self.plan_ws, self.ws, self.gather_ws = (
+            torch.empty(n, dtype=torch.uint8, device=self.device) for _ in range(3))
         n, self.layout = mla_decode_paged_workspace_size(self.c, max_requests, max_blocks,
                                                          block_size)
         self.decode_ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        for ws in (self.ws, self.decode_ws):
+        for ws in (self.plan_ws, self.ws, self.gather_ws, self.decode_ws):
             ws[:256].zero_()           # MLA_OK until a call leaves its own status
 
     def plan(self, new_len, stream=None):
@@ -121,7 +124,8 @@ class MlaPagedCache:
         leaves).  Returns the slot map, the positions and their prefix sums."""
         mla_paged_plan(self.ctx, new_len, self.table, self.ring, self.state, self.ctx, self.state,
                        self.slots, self.positions, self.cu_new, self.B, self.max_blocks,
-                       self.n_blocks, self.block_size, self.capacity, self.ws, stream)
+                       self.n_blocks, self.block_size, self.capacity, self.plan_ws,
+                       stream)
         return self.slots, self.positions, self.cu_new
 
     def append(self, rows, slots=None, stream=None):
@@ -133,7 +137,7 @@ class MlaPagedCache:
     def gather(self, rows_out, cu_ctx, stream=None):
         mla_paged_gather(self.c, self.cache, self.scales, self.table, self.ctx, rows_out, cu_ctx,
                          self.B, self.max_blocks, self.n_blocks, self.block_size,
-                         rows_out.shape[0], self.ws, stream)
+                         rows_out.shape[0], self.gather_ws, stream)
         return rows_out, cu_ctx
 
     def decode(self, q_nope, q_pe, w_kv_b, out, w_o=None, stream=None):
@@ -143,6 +147,15 @@ class MlaPagedCache:
         return out
 
     def check_status(self, stream=None):
-        """The status of the last plan, append or gather, and of the last decode."""
-        mla_check_device_status(self.ws, stream)
-        mla_check_device_status(self.decode_ws, stream)
+        """The statuses of the last plan, append, gather and decode: all are read
+        and cleared, and the first of them that is not MLA_OK is raised.  A plan
+        that failed has done nothing, so the append behind it wrote no row and the
+        decode saw the old lengths."""
+        failed = None
+        for ws in (self.plan_ws, self.ws, self.gather_ws, self.decode_ws):
+            try:
+                mla_check_device_status(ws, stream)
+            except MlaError as e:
+                failed = failed or e
+        if failed:
+            raise failed

@@ -85,3 +85,27 @@ def test_status_before_the_first_call_of_a_kind(lib, monkeypatch):
     pc.plan(torch.zeros(2, dtype=torch.int32), stream=0)
     pc.append(torch.zeros(8, pc.width), stream=0)
     pc.check_status(stream=0)
+
+
+@pytest.mark.parametrize("op,status,name", [
+    ("mla_paged_plan", NO_BLOCKS, "NO_BLOCKS"), ("mla_paged_append", SHAPE, "SHAPE"),
+    ("mla_paged_gather", SHAPE, "SHAPE"), ("mla_decode_paged", SHAPE, "SHAPE")])
+def test_a_failure_in_mid_step_is_seen_at_its_end(lib, op, status, name):
+    pc = cache()
+    lib.outcome[op] = status
+    step(pc)
+    with pytest.raises(P.MlaError, match=name):
+        pc.check_status(stream=0)
+    pc.check_status(stream=0)                     # read once
+    lib.outcome.clear()
+    step(pc)
+    pc.check_status(stream=0)
+
+
+def test_all_statuses_are_read_when_several_failed(lib):
+    pc = cache()
+    lib.outcome.update(mla_paged_plan=NO_BLOCKS, mla_decode_paged=SHAPE)
+    step(pc)
+    with pytest.raises(P.MlaError, match="NO_BLOCKS"):
+        pc.check_status(stream=0)
+    pc.check_status(stream=0)
