@@ -484,7 +484,9 @@ typedef struct mla_paged_layout {
   int32_t split_tokens, max_splits;
 } mla_paged_layout;
 
-/* Workspace bytes mla_decode_paged needs; 0 if the arguments are invalid. */
+/* Workspace bytes mla_decode_paged needs; 0 if the arguments are invalid.  They
+ * never fall as B or max_blocks grows: a workspace of the largest batch and
+ * table serves the smaller ones. */
 MLA_API size_t mla_decode_paged_workspace_size(const mla_config* cfg, int32_t B,
                                                int32_t max_blocks, int32_t block_size,
                                                mla_paged_layout* layout);

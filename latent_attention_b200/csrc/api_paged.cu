@@ -70,12 +70,26 @@ mla::PagedPool pool_of(const mla_config& c, const void* cache, const float* scal
 }
 
 // Tokens per split on CUDA cores: enough splits for some sixteen blocks an SM,
-// between 64 tokens (a block's threads) and 1024 (its partial result, r floats,
-// stays small beside the r-byte rows that it sums).
-constexpr int kSimtSplit = 1024;
+// between 64 tokens (one pass of a block's threads, four a token) and 1024 (its
+// partial result, r floats, stays small beside the r-byte rows that it sums).
+constexpr int kSimtSplit = 1024, kSimtMinSplit = 64;
 int simt_split(const mla_config& c, int64_t B, int64_t max_ctx) {
   const int64_t want = B * c.num_heads * max_ctx / (16ll * mla::device_sms());
-  return (int)std::min<int64_t>(kSimtSplit, std::max<int64_t>(64, (want + 63) / 64 * 64));
+  return (int)std::min<int64_t>(kSimtSplit, std::max<int64_t>(kSimtMinSplit, (want + 63) / 64 * 64));
+}
+
+// Partial results that the workspace holds on CUDA cores: at least B max_splits,
+// and never fewer for a larger B or max_ctx (n), so that a workspace of the
+// largest batch serves every smaller one.  With W = B h n / (16 SMs), B ceil(n /
+// split) is at most
+//   B ceil(n / 1024)                   where the split is 1024,
+//   B + B n / split  otherwise, where split >= floor(W) and split >= 64, thus
+//                    W / split <= 65 / 64:  B + (65 / 64) 16 SMs / h,
+// and always B ceil(n / 64).
+int64_t simt_parts(const mla_config& c, int64_t B, int64_t max_ctx) {
+  const auto splits = [&](int64_t len) { return (max_ctx + len - 1) / len; };
+  const int64_t even = B + 65ll * 16 * mla::device_sms() / (64 * c.num_heads) + 1;
+  return std::max(B * splits(kSimtSplit), std::min(B * splits(kSimtMinSplit), even));
 }
 
 void paged_layout(const mla_config& c, int B, int max_blocks, int block_size,
@@ -99,7 +113,7 @@ void paged_layout(const mla_config& c, int B, int max_blocks, int block_size,
   } else {
     L->split_tokens = simt_split(c, B, max_ctx);
     L->max_splits = (int32_t)((max_ctx + L->split_tokens - 1) / L->split_tokens);
-    parts = (int64_t)B * L->max_splits;
+    parts = simt_parts(c, B, max_ctx);
     L->q_lat = take(B * h * w * es);
     L->q8 = L->plan = -1;
   }

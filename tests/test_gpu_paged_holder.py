@@ -72,3 +72,31 @@ def test_a_plan_that_fails_in_mid_step_is_reported(cuda, captured):
                 assert torch.equal(a, b)
         step.pc.check_status()
     assert step.pc.ctx.tolist() == [16, 16, 8]
+
+
+@pytest.mark.parametrize("B", [1, 19, 20])
+def test_a_workspace_of_the_largest_batch_serves_smaller_ones(cuda, B):
+    """63 blocks of 32: 20 requests run in splits of 128 tokens, 19 in splits
+    of 64, which leave more partial results."""
+    import latent_attention_b200 as L
+    h, bs, mb, n_blocks = F32.num_heads, 32, 63, 64
+    g = torch.Generator().manual_seed(B)
+    cache = torch.randn(n_blocks, bs, F32.kv_lora_rank + F32.qk_rope_head_dim, generator=g)
+    cache = cache.to(torch.float8_e4m3fn).cuda()
+    scales = torch.ones(n_blocks, device="cuda")
+    table = torch.randint(0, n_blocks, (B, mb), dtype=torch.int32, generator=g).cuda()
+    ctx = torch.randint(0, mb * bs + 1, (B,), dtype=torch.int32, generator=g).cuda()
+    qn = torch.randn(B, h, F32.qk_nope_head_dim, generator=g).cuda()
+    qp = torch.randn(B, h, F32.qk_rope_head_dim, generator=g).cuda()
+    w = (0.1 * torch.randn(h * (F32.qk_nope_head_dim + F32.v_head_dim), F32.kv_lora_rank,
+                           generator=g)).cuda()
+    outs = []
+    for sized_for in (20, B):
+        n, _ = L.mla_decode_paged_workspace_size(F32, sized_for, mb, bs)
+        ws = torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
+        out = torch.full((B, h * F32.v_head_dim), 9.0, device="cuda")
+        L.mla_decode_paged(F32, qn, qp, w, cache, scales, table, ctx, B, mb, n_blocks, bs, None,
+                           out, ws)
+        L.mla_check_device_status(ws)
+        outs.append(out)
+    assert torch.equal(*outs) and not torch.isnan(outs[0]).any()
