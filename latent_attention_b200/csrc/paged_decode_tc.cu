@@ -60,6 +60,7 @@
 // slower), blocks' lines asked for ahead in L2 (the same).
 #include "paged.cuh"
 #include "paged_slices.cuh"
+#include "ring_drain.cuh"
 #include "sm100.cuh"
 #include "tc.h"
 
@@ -120,6 +121,7 @@ struct Shared {
       p_full[K::NP], pv_done[K::NP];
   uint32_t tmem_base;
   int abort_flag;
+  int issued[4];                           // ring positions filled: boxes (warp 0, warp 2), rope, queries
 };
 template <int NH>
 constexpr int smem_bytes() { return Cfg<NH>::OFF_SH + (int)sizeof(Shared<NH>); }
@@ -383,19 +385,11 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
       tma_load_2d(smem + K::OFF_C + slot * BOX + (i << p.lbs) * 128, &tmC, 64 * a, ids[i] << p.lbs,
                   &sh.c_full[slot]);
   };
-  // after an abort: the copies in flight (one fill a slot at most, of this pass
-  // over the ring before `slot`, of the pass before from it on) land before the
-  // block ends
-  const auto drain = [&](int slot, uint32_t ph) {
-    int given_up = 0;
-    for (int i = 0; i < NS; ++i)
-      mbar_wait(&sh.c_full[i], (i < slot ? ph ^ 1 : ph) & 1, &given_up, nullptr);
-  };
-
   if (warp == 0) {
     // ---------------- TMA of the rope boxes and of the first two boxes
     if (elect_one()) {
       int slot = 0, rs = 0, g = 0, n = 0;
+      int issued = 0, ropes = 0;              // ring positions behind this warp's last loads
       uint32_t ph = 1, rph = 1;               // parities of the empty barriers
       for (; !c.done; ++g) {
         if (c.j == 0) n = tokens(c);
@@ -409,22 +403,26 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
         for (int i = 0; i < blocks; ++i)
           tma_load_2d(smem + K::OFF_R + rs * RBOX + (i << p.lbs) * DR, &tmCr, R / 2,
                       ids[i] << p.lbs, &sh.r_full[rs]);
+        ++ropes;
         if (++rs == NR) { rs = 0; rph ^= 1; }
         if (!mbar_wait(&sh.c_empty[slot], ph, abort_v, p.status)) break;
         load_box(0, slot, blocks, ids);
+        issued = 4 * g + 1;
         if (++slot == NS) { slot = 0; ph ^= 1; }
         if (!mbar_wait(&sh.c_empty[slot], ph, abort_v, p.status)) break;
         load_box(1, slot, blocks, ids);
+        issued = 4 * g + 2;
         slot += 3;
         if (slot >= NS) { slot -= NS; ph ^= 1; }
         advance(c);
       }
-      if (*abort_v) drain(slot, ph);
+      sh.issued[0] = issued;
+      sh.issued[2] = ropes;
     }
   } else if (warp == 1) {
     // ---------------- the segments' queries, S of every chunk
     if (elect_one()) {
-      int slot = 0, rs = 0, g = 0;
+      int slot = 0, rs = 0, g = 0, queries = 0;
       uint32_t ph = 0, rph = 0;
       const uint32_t qb = smem_u32(smem);
       const uint64_t dq = desc_kmajor_sw128(qb), dqr = desc_kmajor_sw64(qb + 4 * K::QBOX);
@@ -437,6 +435,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
           const int y = (c.s.b * p.groups + hg) * 2 * NH;
           tma_load_2d(smem + 4 * K::QBOX, &tmQr, R / 2, y, &sh.q_full);
           for (int a = 0; a < 4; ++a) tma_load_2d(smem + a * K::QBOX, &tmQ, 64 * a, y, &sh.q_full);
+          ++queries;
           if (!mbar_wait(&sh.q_full, c.kk & 1, abort_v, p.status)) break;
         }
         const int sls = g % NSL;
@@ -466,6 +465,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
         if (c.j == c.s.nch - 1) mma_commit(&sh.q_free);
         advance(c);
       }
+      sh.issued[3] = queries;
     }
   } else if (warp == 3) {
     // ---------------- PV of every chunk
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
       ++lg;
     };
     look_up();
-    int slot = 2;
+    int slot = 2, issued = 0;
     uint32_t ph = 1;
     for (int g = 0; !c.done; ++g) {
       if (c.j == 0) n = tokens(c);
@@ -572,6 +572,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
         ok = warp_wait(&sh.c_empty[slot], ph, abort_v, p.status);
         if (!ok) break;
         if (elect_one()) load_box(a, slot, blocks, sh.ids[g % GR]);
+        issued = 4 * g + a + 1;
         __syncwarp();
         slot += a == 2 ? 1 : 3;
         if (slot >= NS) { slot -= NS; ph ^= 1; }
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
       while (lg <= g + AHEAD && (pending || !look.done)) look_up();
       advance(c);
     }
-    if (lane == 0 && *abort_v) drain(slot, ph);
+    if (lane == 0) sh.issued[1] = issued;
   } else {
     // ---------------- softmax: thread = token, group = HPG heads
     const int grp = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
@@ -856,6 +857,21 @@ __global__ void __launch_bounds__(Cfg<NH>::NTHREADS, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_v) {
+    // a wait ran out somewhere: the copies still in flight (boxes by warps 0 and
+    // 2, rope, queries) land before the block leaves its shared memory
+    int given_up = 0;
+    const auto wait = [&](uint64_t* full) {
+      return [=, &given_up](int slot, uint32_t parity) {
+        mbar_wait(&full[slot], parity, &given_up, nullptr);
+      };
+    };
+    const int i0 = sh.issued[0], i2 = sh.issued[1];
+    drain_ring(max(i0, i2), NS, [=](int f) { return f < ((f & 3) < 2 ? i0 : i2); },
+               wait(sh.c_full));
+    drain_ring(sh.issued[2], NR, [](int) { return true; }, wait(sh.r_full));
+    drain_ring(sh.issued[3], 1, [](int) { return true; }, wait(&sh.q_full));
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, K::TM_COLS);
