@@ -12,6 +12,7 @@
 // to memory.
 #include <algorithm>
 
+#include "ring_drain.cuh"
 #include "sm100.cuh"
 #include "tc.h"
 
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(NT) paged_oproj_kernel(const __grid_constant__
     for (int i = 0; i < min(n, stages); ++i) load_w(i, i);
   griddep_wait();
   griddep_launch_dependents();
+  int issued = 0;                        // stages filled whole, by thread 32
   if (warp == 1) {
     if (lane == 0) {
       int s = 0;
@@ -125,6 +127,7 @@ __global__ void __launch_bounds__(NT) paged_oproj_kernel(const __grid_constant__
           load_w(i, s);
         }
         load_o(i, s);
+        issued = i + 1;
         if (++s == stages) { s = 0; ph ^= 1; }
       }
     }
@@ -154,6 +157,15 @@ __global__ void __launch_bounds__(NT) paged_oproj_kernel(const __grid_constant__
   // all threads: row n0 + t of the tile, into shared memory as [sequence][row]
   // (after a timeout the cluster goes on together; the status word says so)
   mbar_wait(&done, 0, abort_v, p.status);
+  // a wait ran out somewhere: what is still in flight lands before the ring's
+  // memory is the sums' (no weights are on their way alone: the first stages get
+  // their o without a wait, the others both at once)
+  if (t == 32 && *abort_v) {
+    int given_up = 0;
+    drain_ring(issued, stages, [](int) { return true; }, [&](int s, uint32_t parity) {
+      mbar_wait(&full[s], parity, &given_up, nullptr);
+    });
+  }
   tc_fence_after();
   __syncthreads();
   float* sums = reinterpret_cast<float*>(smem);
