@@ -416,9 +416,10 @@ MLA_API size_t mla_paged_workspace_size(int32_t n_blocks);
  *                capacity is 0
  *   cu_new       [B + 1]
  * All or nothing: when the ring or the capacity is too small (status
- * MLA_ERR_NO_BLOCKS) or a length or the ring's state is out of range
- * (MLA_ERR_SHAPE), tables, ring, lengths and state stay as they were, cu_new
- * is zero and every slot is -1.
+ * MLA_ERR_NO_BLOCKS) or a length, the ring's state or an id is out of range
+ * that the step takes from the ring, gives back to it or writes new tokens
+ * behind (MLA_ERR_SHAPE), tables, ring, lengths and state stay as they were,
+ * cu_new is zero and every slot is -1.
  */
 MLA_API mla_status mla_paged_plan(const int32_t* ctx_len, const int32_t* new_len,
                                   int32_t* block_table, int32_t* free_ring,

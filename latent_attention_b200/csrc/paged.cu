@@ -33,11 +33,14 @@ using namespace paged;
 // many slots are left to a second grid, which finds the prefixes in the
 // workspace.  A new token's block is looked up where it comes from, the old
 // table or the ring, so nothing waits for the table to be written.
-// All or nothing: if anything is out of range or the ring or the slot map is
-// too short, every output says "nothing happened".
+// All or nothing: if anything is out of range (a length, the ring's state, a
+// block id that the step takes, gives back or fills further) or the ring or the
+// slot map is too short, every output says "nothing happened".  So all ids are
+// read before anything is written.
 // It moves a few KB (a step of 256 requests) to some MB (prompts): a launch and
-// three dependent trips to memory are its time, 5.9 us for a step of 256
-// requests, 6.5 us for 61 prompts of 4000 tokens on average in blocks of 16.
+// three dependent trips to memory are its time, 5.7 us for a step of 256
+// requests, 8.1 us for 61 prompts of 4000 tokens on average in blocks of 16 (1.6
+// of it the look at 15000 ids by one block), 47 us for 8192 requests.
 
 __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
 #pragma unroll
@@ -65,39 +68,35 @@ __device__ __forceinline__ PlanSums sums_at(int32_t* base, int B) {
   return s;
 }
 
-__device__ __forceinline__ int wrap(int64_t i, int n) { return (int)(i >= n ? i - n : i); }
+// (n_blocks is below 2^27: sums of two ring positions are ints)
+__device__ __forceinline__ int wrap(int i, int n) { return i >= n ? i - n : i; }
 
-// The step's entries and slots (tn < 0: nothing happened), by threads first,
-// first + step, ...
-__device__ __forceinline__ void fill(const PlanArgs& a, const PlanSums& s, int first, int step) {
-  const int n = a.n_blocks;
-  for (int i = first; i < s.ta; i += step) {
-    const int b = request_of(s.add_end, a.B, i);
-    const int v = a.ring[wrap((int64_t)s.head + i, n)];
-    if (v < 0 || v >= n) atomicOr(a.status, kStatusBadPage);
-    a.table[(int64_t)b * a.max_blocks + s.held[b] + i - (b ? s.add_end[b - 1] : 0)] = v;
-  }
-  for (int i = first; i < s.tg; i += step) {
-    const int b = request_of(s.give_end, a.B, i);
-    const int v = a.table[(int64_t)b * a.max_blocks + i - (b ? s.give_end[b - 1] : 0)];
-    if (v < 0 || v >= n) atomicOr(a.status, kStatusBadPage);
-    a.ring[wrap(wrap((int64_t)s.head + s.count, n) + (int64_t)i, n)] = v;
-  }
-  for (int i = first; i < a.capacity; i += step) {
-    int slot = -1, at = 0;
-    if (i < s.tn) {
-      const int b = request_of(s.new_end, a.B, i);
-      at = s.after[b] - (s.new_end[b] - i);      // the request's last new token is after[b] - 1
-      const int j = at / a.bs, had = s.held[b];
-      const int blk =
-          j < had ? a.table[(int64_t)b * a.max_blocks + j]
-                  : a.ring[wrap((int64_t)s.head + (b ? s.add_end[b - 1] : 0) + j - had, n)];
-      if (blk >= 0 && blk < n) slot = blk * a.bs + at % a.bs;
-      else atomicOr(a.status, kStatusBadPage);
-    }
-    a.slots[i] = slot;
-    if (a.pos) a.pos[i] = at;
-  }
+// Entry i of the step's work: the i-th block taken, the i-th given back, the
+// block and the position of the i-th new token; where each goes.
+__device__ __forceinline__ int taken(const PlanArgs& a, const PlanSums& s, int i) {
+  return a.ring[wrap(s.head + i, a.n_blocks)];
+}
+__device__ __forceinline__ void put_taken(const PlanArgs& a, const PlanSums& s, int i, int id) {
+  const int b = request_of(s.add_end, a.B, i);
+  a.table[(int64_t)b * a.max_blocks + s.held[b] + i - (b ? s.add_end[b - 1] : 0)] = id;
+}
+__device__ __forceinline__ int given(const PlanArgs& a, const PlanSums& s, int i) {
+  const int b = request_of(s.give_end, a.B, i);
+  return a.table[(int64_t)b * a.max_blocks + i - (b ? s.give_end[b - 1] : 0)];
+}
+__device__ __forceinline__ void put_given(const PlanArgs& a, const PlanSums& s, int i, int id) {
+  a.ring[wrap(wrap(s.head + s.count, a.n_blocks) + i, a.n_blocks)] = id;
+}
+__device__ __forceinline__ int block_of(const PlanArgs& a, const PlanSums& s, int i, int& at) {
+  const int b = request_of(s.new_end, a.B, i);
+  at = s.after[b] - (s.new_end[b] - i);          // the request's last new token is after[b] - 1
+  const int j = at / a.bs, had = s.held[b];
+  return j < had ? a.table[(int64_t)b * a.max_blocks + j]
+                 : taken(a, s, (b ? s.add_end[b - 1] : 0) + j - had);
+}
+__device__ __forceinline__ void put_slot(const PlanArgs& a, int i, int id, int at) {
+  a.slots[i] = id < 0 ? -1 : id * a.bs + at % a.bs;
+  if (a.pos) a.pos[i] = at;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int alone) {
@@ -107,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int alon
   __shared__ int32_t s_head, s_count;
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
-  PlanSums s = sums_at(alone ? sm : a.sums + 8, a.B);
+  PlanSums s = sums_at(sm, a.B);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   if (t == 0) {
     s_head = a.state[0];
@@ -115,13 +114,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int alon
     a.status[0] = a.status[1] = 0;
   }
   const int per = (a.B + kPlanThreads - 1) / kPlanThreads, b0 = t * per, b1 = min(b0 + per, a.B);
+  const int lbs = __ffs(a.bs) - 1;
   int64_t add = 0, give = 0, fresh = 0;
-  bool bad = false;
+  bool bad = false, bad_id = false;
+  const auto look = [&](int id) { bad_id |= id < 0 || id >= a.n_blocks; };
+  int part = 0;                                  // the id of a part-filled block that goes on
   for (int b = b0; b < b1; ++b) {
     const int64_t c = a.ctx[b], n = a.fresh[b];
     const int64_t grow = n > 0 ? n : 0;
-    int64_t hb = (c + a.bs - 1) / a.bs, wb = (c + grow + a.bs - 1) / a.bs;
+    int64_t hb = (c + a.bs - 1) >> lbs, wb = (c + grow + a.bs - 1) >> lbs;
     if (c < 0 || n < -1 || wb > a.max_blocks) { bad = true; hb = wb = 0; }
+    if (!alone) {                                // (used one request later, or behind the scan)
+      look(part);
+      part = n > 0 && hb > 0 && (c & (a.bs - 1)) ? a.table[(int64_t)b * a.max_blocks + hb - 1] : 0;
+    }
     add += n < 0 ? 0 : wb - hb;
     give += n < 0 ? hb : 0;
     fresh += grow;
@@ -151,42 +157,94 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int alon
   s.count = s_count;
   const bool broken = any_bad || s.head < 0 || s.head >= n || s.count < 0 || s.count > n ||
                       s.count + tg > n;          // more blocks than the pool has
-  const bool ok = !broken && ta <= s.count && tn <= a.capacity;
-  s.ta = ok ? (int)ta : 0;
-  s.tg = ok ? (int)tg : 0;
-  s.tn = ok ? (int)tn : 0;
-  // exclusive prefix of this thread's requests (int: used only when ok)
+  const bool fits = !broken && ta <= s.count && tn <= a.capacity;
+  s.ta = fits ? (int)ta : 0;
+  s.tg = fits ? (int)tg : 0;
+  s.tn = fits ? (int)tn : 0;
+  // exclusive prefix of this thread's requests (int: used only when all fits)
   const int xa = (int)(warp_sum[0][warp] + ia - add), xg = (int)(warp_sum[1][warp] + ig - give),
             xn = (int)(warp_sum[2][warp] + in - fresh);
   for (int b = b0; b < b1; ++b) {
     s.add_end[b] += xa;
     s.give_end[b] += xg;
     s.new_end[b] += xn;
+  }
+  __syncthreads();
+  // The ids of blocks that change hands or take new tokens.  A block alone keeps
+  // what it read for the writes (kHeld entries of each kind a thread; every block
+  // taken has a slot, so its id is looked at there).
+  constexpr int kHeld = kPlanOneBlock / kPlanThreads;
+  constexpr int kAsk = 8;                        // (16: the same; without: 8.9 us for the prompts)
+  int id[kHeld], at[kHeld], take[kHeld], back[kHeld];
+  if (alone) {
+#pragma unroll
+    for (int q = 0; q < kHeld; ++q) {
+      const int i = t + q * kPlanThreads;
+      id[q] = -1;
+      at[q] = take[q] = back[q] = 0;
+      if (i < s.ta) take[q] = taken(a, s, i);
+      if (i < s.tn) look(id[q] = block_of(a, s, i, at[q]));
+      if (i < s.tg) look(back[q] = given(a, s, i));
+    }
+    for (int i = t + kHeld * kPlanThreads; i < s.tg; i += kPlanThreads) look(given(a, s, i));
+  } else {
+    look(part);
+    for (int i = t; i < s.ta; i += kAsk * kPlanThreads) {
+      int v[kAsk];
+#pragma unroll
+      for (int q = 0; q < kAsk; ++q)
+        v[q] = i + q * kPlanThreads < s.ta ? taken(a, s, i + q * kPlanThreads) : 0;
+#pragma unroll
+      for (int q = 0; q < kAsk; ++q) look(v[q]);
+    }
+    for (int i = t; i < s.tg; i += kPlanThreads) look(given(a, s, i));
+  }
+  const bool broken_id = __syncthreads_or(bad_id), ok = fits && !broken_id;
+  if (!ok) s.ta = s.tg = s.tn = 0;
+  for (int b = b0; b < b1; ++b) {
     a.cu[b + 1] = ok ? s.new_end[b] : 0;
     const int32_t was = a.ctx[b];                // before ctx_out, which may be ctx
     a.ctx_out[b] = ok ? s.after[b] : was;
   }
   if (t == 0) {
     a.cu[0] = 0;
-    a.state_out[0] = ok ? wrap((int64_t)s.head + ta, n) : s.head;
+    a.state_out[0] = ok ? wrap(s.head + (int)ta, n) : s.head;
     a.state_out[1] = ok ? (int)(s.count - ta + tg) : s.count;
-    if (!ok) atomicOr(a.status, broken ? kStatusBadPage : kStatusNoBlocks);
+    if (!ok) atomicOr(a.status, broken || broken_id ? kStatusBadPage : kStatusNoBlocks);
     if (!alone) {
       a.sums[0] = s.head; a.sums[1] = s.count; a.sums[2] = s.ta; a.sums[3] = s.tg;
       a.sums[4] = s.tn;
     }
   }
-  __syncthreads();
-  if (alone) fill(a, s, t, kPlanThreads);
+  if (!alone) {
+    for (int i = t; i < 5 * a.B; i += kPlanThreads) a.sums[8 + i] = sm[i];
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) {
+    const int i = t + q * kPlanThreads;
+    if (i < s.ta) put_taken(a, s, i, take[q]);
+    if (i < s.tg) put_given(a, s, i, back[q]);
+    if (i < a.capacity) put_slot(a, i, ok ? id[q] : -1, ok ? at[q] : 0);
+  }
+  for (int i = t + kHeld * kPlanThreads; i < s.tg; i += kPlanThreads)
+    put_given(a, s, i, given(a, s, i));
 }
 
-// Entries and slots on their own grid.
+// Entries and slots on their own grid; the ids have been checked.
 __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(PlanArgs a) {
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
   PlanSums s = sums_at(a.sums + 8, a.B);
   s.head = a.sums[0]; s.count = a.sums[1]; s.ta = a.sums[2]; s.tg = a.sums[3]; s.tn = a.sums[4];
-  fill(a, s, blockIdx.x * kFillThreads + threadIdx.x, gridDim.x * kFillThreads);
+  const int first = blockIdx.x * kFillThreads + threadIdx.x, step = gridDim.x * kFillThreads;
+  for (int i = first; i < s.ta; i += step) put_taken(a, s, i, taken(a, s, i));
+  for (int i = first; i < s.tg; i += step) put_given(a, s, i, given(a, s, i));
+  for (int i = first; i < a.capacity; i += step) {
+    int id = -1, at = 0;
+    if (i < s.tn) id = block_of(a, s, i, at);
+    put_slot(a, i, id, at);
+  }
 }
 
 // ----------------------------------------------------------------- append
@@ -551,7 +609,7 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const bool alone = a.capacity <= kPlanOneBlock;
   const cudaError_t e1 = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads),
-                                    alone ? 5 * 4 * (size_t)a.B : 0, st, a, (int)alone);
+                                    5 * 4 * (size_t)a.B, st, a, (int)alone);
   count_launches();
   if (e1 != cudaSuccess || alone) return e1;
   const int grid = std::min((a.capacity + kFillThreads - 1) / kFillThreads, 8 * 148);

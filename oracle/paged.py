@@ -58,15 +58,22 @@ def plan(ctx, new, table, ring, state, block_size, capacity):
     blocks = lambda n: -(-n // block_size)
     broken = not (0 <= head < n_blocks and 0 <= count <= n_blocks)
     take, give, total = 0, 0, 0
-    for c, n in zip(ctx, new):
+    bad_id = lambda v: not 0 <= int(v) < n_blocks
+    ids = []                                       # of blocks given back or filled further
+    for b, (c, n) in enumerate(zip(ctx, new)):
         if c < 0 or n < -1 or blocks(c + max(n, 0)) > width:
             broken = True
             continue
         take += 0 if n < 0 else blocks(c + n) - blocks(c)
         give += blocks(c) if n < 0 else 0
         total += max(n, 0)
+        ids += list(table[b, :blocks(c)]) if n < 0 else \
+            [table[b, c // block_size]] if n > 0 and c % block_size else []
     broken = broken or count + give > n_blocks
     short = take > count or total > capacity
+    if not broken and not short:
+        ids += [ring[(head + i) % n_blocks] for i in range(take)]
+        broken = any(bad_id(v) for v in ids)
     res = dict(table=table, ring=ring, ctx=np.array(ctx), state=np.array([head, count]),
                cu=np.zeros(len(ctx) + 1, np.int64), slots=np.full(capacity, -1, np.int64),
                pos=np.zeros(capacity, np.int64),
