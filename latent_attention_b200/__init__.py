@@ -288,13 +288,13 @@ def mla_decode_absorbed_noalloc(cfg, q_nope, q_pe, w_kv_b, latent_cache, cu_ctx,
 def _torch():
     global _T, _I32, _F32, _FP8, _U8, _DTYPES, _raw_stream, _current_device
     import torch
-    _T, _I32, _F32 = torch, torch.int32, torch.float32
+    _I32, _F32 = torch.int32, torch.float32
     _FP8, _U8 = torch.float8_e4m3fn, torch.uint8
     _DTYPES = {MLA_BF16: torch.bfloat16, MLA_F32: torch.float32}
     # without torch.cuda's bookkeeping around them, where torch has them
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-    return torch
+    _T = torch        # last: another thread that sees it finds the others
 
 
 _T = None
