@@ -244,8 +244,9 @@ __global__ void __launch_bounds__(NT) paged_query_kernel(const __grid_constant__
     if (rr < n)
       pe2 = reinterpret_cast<const uint2*>(p.q_pe + ((int64_t)(base + rr) * p.h + hh) * DR)[part];
     for (int kc = 0; kc < p.dn; kc += 128) {
-      // 128 rows of W_UK[h]; past dn they are W_UV's and meet zeros of q.  Up
-      // to 128 rows they stay for all rounds.
+      // 128 rows of W_UK[h]; past dn they are W_UV's and the next head's, and
+      // become zeros (to meet zeros of q is not enough for an infinity or NaN).
+      // Up to 128 rows they stay for all rounds.
       const bool load = round == 0 || p.dn > 128;
       if (t == 0 && load) {
         mbar_arrive_expect_tx(&full, W_BYTES);
@@ -260,7 +261,17 @@ __global__ void __launch_bounds__(NT) paged_query_kernel(const __grid_constant__
                    q4.w);
       __syncthreads();
       // (after a timeout the block goes on; the status word says so)
-      if (load) mbar_wait(&full, phase++ & 1, &abort_flag, p.status);
+      if (load) {
+        mbar_wait(&full, phase++ & 1, &abort_flag, p.status);
+        const int past = kc + 128 - p.dn;
+        if (past > 0) {
+          for (int k = t; k < 64 * past; k += NT)
+            st_shared_v4(wbase + (k & 7) * WBOX + (127 - (k >> 6)) * 128 + ((k >> 3) & 7) * 16, 0u,
+                         0u, 0u, 0u);
+          fence_proxy_async();             // before the loads that come into their place
+          __syncthreads();
+        }
+      }
 #pragma unroll 2
       for (int ks = 0; ks < 8; ++ks) {
         uint32_t a[2][4], b[2][4];
