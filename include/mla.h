@@ -415,6 +415,7 @@ MLA_API size_t mla_paged_workspace_size(int32_t n_blocks);
  *   slot_map, positions  [capacity]; positions may be NULL, both may be when
  *                capacity is 0
  *   cu_new       [B + 1]
+ * positions are the rows of the RoPE tables for the new tokens' q_pe and k_pe.
  * All or nothing: when the ring or the capacity is too small (status
  * MLA_ERR_NO_BLOCKS) or a length, the ring's state or an id is out of range
  * that the step takes from the ring, gives back to it or writes new tokens
@@ -457,8 +458,9 @@ MLA_API mla_status mla_paged_append(const mla_config* cfg, const void* rows,
 
 /*
  * mla_paged_gather -- the cached rows of all requests back to back in
- * cfg->dtype (the history a chunked prefill uncompresses, or a contiguous
- * cache for mla_decode_absorbed).
+ * cfg->dtype: the history of a chunked prefill (mla_prefill_chunked takes one
+ * T_past for all its sequences, so requests of unequal lengths go in one at a
+ * time, from row cu_ctx[b] on), or a contiguous cache for mla_decode_absorbed.
  *
  *   rows_out  [capacity, kv_lora_rank + rope]: row cu_ctx[b] + j is token j of
  *             request b; rows from cu_ctx[B] on are left alone.  NULL when
