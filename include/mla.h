@@ -506,6 +506,19 @@ MLA_API size_t mla_decode_paged_workspace_size(const mla_config* cfg, int32_t B,
  * shares them keeps the count).  On tensor cores latent values must stay below
  * 2^80 in magnitude: weights up to 2^24 relative to a segment's first token
  * multiply them in fp32.
+ *
+ * Precision.  The bytes enter as they are; scores, softmax statistics and all
+ * sums are fp32 and out is rounded once.  On tensor cores what multiplies the
+ * bytes is a sum of two e4m3 terms, 8 significant bits as bf16 has:
+ *   [q_lat | q_pe] of a head to 2^-8 of each value, or 2^-17 of the head's
+ *     largest where that is more;
+ *   a weight times its block's scale, p_j 2^e, to 2^-8 + 2^-11 of itself, or
+ *     2^-17 of the largest among the 32 tokens 32 k .. 32 k + 31 of the request
+ *     where that is more.  (Blocks of 16 share such a group: rows whose p_j 2^e
+ *     is 2^-17 of a neighbour block's no longer count.)
+ * o_lat and o keep 16 significant bits on their way into the next product.  On
+ * CUDA cores everything is fp32, but that with MLA_BF16 q_lat and, before an
+ * output projection, o are rounded to bf16 between kernels.
  */
 MLA_API mla_status mla_decode_paged(const mla_config* cfg, const void* q_nope, const void* q_pe,
                                     const void* w_kv_b, const void* cache, const float* scales,

@@ -4,6 +4,9 @@
 //   s_j = scale (q_lat . c_j + q_pe . kpe_j); partial softmax
 //   statistics and sums over splits of the context           (split kernel)
 //   log-sum-exp merge of the splits, o = W_UV[h] o_lat       (merge kernel)
+// Between the kernels q_lat, and o before an output projection, are in the
+// model's type: with bf16 that is 2^-8 of each value, the precision that the
+// query and the output have anyway, and the projections behind read bf16.
 // Every head reads the rows again (from L2, mostly) and the products are fp32
 // FMAs, so this is the form for what the tensor cores do not take: fp32 and
 // other widths.  8 requests of up to 2000 tokens, 4 heads of a small fp32 layer:
