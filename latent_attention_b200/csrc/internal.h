@@ -148,6 +148,9 @@ struct PlanArgs {
   int32_t* sums;                   // [8 + 5 B]: the prefixes, where a second grid needs them
 };
 
+// SMs of a B200: what the paged launch rules count with (and were measured on).
+constexpr int kSMs = 148;
+
 // Requests a paged call takes at most: every scan over them fits the shared
 // memory of one block.
 constexpr int kMaxRequests = 8192;

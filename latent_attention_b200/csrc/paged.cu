@@ -612,7 +612,7 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
                                     5 * 4 * (size_t)a.B, st, a, (int)alone);
   count_launches();
   if (e1 != cudaSuccess || alone) return e1;
-  const int grid = std::min((a.capacity + kFillThreads - 1) / kFillThreads, 8 * 148);
+  const int grid = std::min((a.capacity + kFillThreads - 1) / kFillThreads, 8 * kSMs);
   count_launches();
   return launch_pdl(plan_fill_kernel, dim3(grid), dim3(kFillThreads), 0, st, a);
 }
@@ -624,11 +624,11 @@ cudaError_t launch_paged_append(int dtype, const void* rows, const int32_t* slot
   // SM (4096 rows in 64 runs 6.2 us, against 10.2 with four windows an SM, whose
   // empty blocks are in the way, and 11.0 with 256 threads).  Beyond: 256 threads
   // and four windows an SM, whose blocks overlap each other's trips to memory.
-  const bool few = n_rows < 2 * 148 * pool.bs;
-  const int windows = few ? 148 : 4 * 148;
+  const bool few = n_rows < 2 * kSMs * pool.bs;
+  const int windows = few ? kSMs : 4 * kSMs;
   const int window = std::min((n_rows + windows - 1) / windows, pool.bs);
   const int grid = (n_rows + window - 1) / window;
-  static_assert(kAppendScan < 2 * 148 * 16, "256-thread blocks take claims");
+  static_assert(kAppendScan < 2 * kSMs * 16, "256-thread blocks take claims");
   if (n_rows <= kAppendScan) claims = nullptr;   // (at most 4096 / 16 blocks)
   count_launches();
   const auto go = [&](auto kernel, auto* p, int nt) {
@@ -649,7 +649,7 @@ cudaError_t launch_paged_gather(int dtype, const PagedPool& pool, const int32_t*
                                 const int32_t* ctx, void* rows, int32_t* cu, int B,
                                 int max_blocks, int capacity, uint32_t* status, cudaStream_t st) {
   const int tiles = (capacity + kGatherRows - 1) / kGatherRows;
-  const int grid = tiles < 8 * 148 ? (tiles > 0 ? tiles : 1) : 8 * 148;
+  const int grid = tiles < 8 * kSMs ? (tiles > 0 ? tiles : 1) : 8 * kSMs;
   const size_t smem = 4 * (size_t)B;
   count_launches();
   if (dtype == MLA_F32)

@@ -43,23 +43,6 @@ int smem_of(int bn) {
   return std::max(stages_of(bn) * stage_bytes(bn), bn * 132 * 4) + 1024;
 }
 
-template <bool USE>
-__device__ __forceinline__ void mma_keep(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t acc) {
-  if (USE)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16.collector::a::lastuse [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16.collector::a::fill [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
 // Block (x, y, z): weight rows 128 x ..., piece y of K (the cluster), sequences
 // bn z ...
 __global__ void __launch_bounds__(NT) paged_oproj_kernel(const __grid_constant__ CUtensorMap tmW,
@@ -144,8 +127,8 @@ __global__ void __launch_bounds__(NT) paged_oproj_kernel(const __grid_constant__
         const uint64_t dl = desc_kmajor_sw128(at + ABOX + p.bn * 128);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          mma_keep<false>(tbase, da + 2 * k, dh + 2 * k, idesc, (i | k) != 0);
-          mma_keep<true>(tbase, da + 2 * k, dl + 2 * k, idesc, 1);
+          mma_bf16_keep<false>(tbase, da + 2 * k, dh + 2 * k, idesc, (i | k) != 0);
+          mma_bf16_keep<true>(tbase, da + 2 * k, dl + 2 * k, idesc, 1);
         }
         mma_commit(&empty[s]);
         if (++s == stages) { s = 0; ph ^= 1; }
@@ -171,13 +154,7 @@ __global__ void __launch_bounds__(NT) paged_oproj_kernel(const __grid_constant__
   float* sums = reinterpret_cast<float*>(smem);
   for (int c = 0; c < p.bn; c += 16) {
     uint32_t v[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-          "=r"(v[14]), "=r"(v[15])
-        : "r"(tbase + ((uint32_t)(warp * 32) << 16) + c));
+    tmem_ld16(tbase + ((uint32_t)(warp * 32) << 16) + c, v);
     tmem_wait_ld();
 #pragma unroll
     for (int k = 0; k < 16; ++k) sums[(c + k) * 132 + t] = __uint_as_float(v[k]);
@@ -226,7 +203,7 @@ cudaError_t launch_paged_oproj(const void* o, const void* o_lo, const void* w_o,
   const int tiles = (hidden + 127) / 128, rows = (B + p.bn - 1) / p.bn;
   // pieces of K: blocks for every SM, eight chunks a piece at least
   int pieces = 1;
-  while (pieces < 8 && 2 * pieces * tiles * rows <= 148 && p.chunks >= 16 * pieces) pieces *= 2;
+  while (pieces < 8 && 2 * pieces * tiles * rows <= kSMs && p.chunks >= 16 * pieces) pieces *= 2;
   CUtensorMap tmW, tmO, tmL;
   const uint64_t str[1] = {(uint64_t)K * 2};
   const uint64_t wd[2] = {(uint64_t)K, (uint64_t)hidden}, od[2] = {(uint64_t)K, (uint64_t)B};

@@ -42,7 +42,7 @@ constexpr int MB = 32;                   // sequences in a round
 // then read by several), more beyond, up to four.
 int rounds_of(const PagedDecodeArgs& a) {
   const int64_t blocks = (int64_t)a.h * ((a.B + MB - 1) / MB);
-  return (int)std::min<int64_t>(4, (blocks + 147) / 148);
+  return (int)std::min<int64_t>(4, (blocks + kSMs - 1) / kSMs);
 }
 constexpr int WBOX = 128 * 128;          // 128 rows of 64 bf16 weights
 constexpr int W_BYTES = 8 * WBOX;
@@ -374,24 +374,6 @@ constexpr int O_SMEM = W_BYTES + 2 * A_BYTES + RED + 1024;
 constexpr int kUnits = 512;                // most units (host side: tc_paged_plan)
 constexpr int kShared = 8;                 // more partials than this: the whole block merges
 
-// D (+)= A B^T; the weights A stay in the collector for the second term.
-template <bool LAST>
-__device__ __forceinline__ void mma_keep(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t acc) {
-  if (LAST)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16.collector::a::lastuse [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16.collector::a::fill [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
 __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant__ CUtensorMap tmW,
                                                           OutputParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -580,8 +562,8 @@ __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant_
           const uint64_t dl = desc_kmajor_sw128(abase + A_BYTES + box * MB * 128);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            mma_keep<false>(tbase, da + 2 * k, dh + 2 * k, idesc, (box | k) != 0);
-            mma_keep<true>(tbase, da + 2 * k, dl + 2 * k, idesc, 1);
+            mma_bf16_keep<false>(tbase, da + 2 * k, dh + 2 * k, idesc, (box | k) != 0);
+            mma_bf16_keep<true>(tbase, da + 2 * k, dl + 2 * k, idesc, 1);
           }
         }
         mma_commit(&done);
@@ -595,13 +577,7 @@ __global__ void __launch_bounds__(NT) paged_output_kernel(const __grid_constant_
         const int half = warp >> 2, col = nc + (warp & 3) * 32 + lane;
         if (16 * half < n) {
           uint32_t v[16];
-          asm volatile(
-              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-              "%10, %11, %12, %13, %14, %15}, [%16];"
-              : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
-                "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]),
-                "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-              : "r"(tbase + ((uint32_t)((warp & 3) * 32) << 16) + 16 * half));
+          tmem_ld16(tbase + ((uint32_t)((warp & 3) * 32) << 16) + 16 * half, v);
           tmem_wait_ld();
           if (col < p.dv) {
 #pragma unroll
