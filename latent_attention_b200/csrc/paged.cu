@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : sizeof(T) == 4 ? 4 : 3)
 // the lengths into shared memory and takes tiles of kGatherRows rows: the
 // tile's source rows are looked up once, then a thread takes one 16-byte
 // column of every R-th row, four loads in flight.  Memory bounds it (1152 bytes
-// written and 576 read a token in bf16): 556900 tokens, 0.96 GB, take 160 us, 6.0
+// written and 576 read a token in bf16): 556900 tokens, 0.96 GB, take 164 us, 5.9
 // TB/s; 8192 tokens 4.8 us, where looking up rows before bytes is two trips.
 constexpr int kGatherThreads = 288, kGatherRows = 32, kGatherFly = 4;
 

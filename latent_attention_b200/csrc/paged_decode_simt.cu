@@ -10,7 +10,7 @@
 // Every head reads the rows again (from L2, mostly) and the products are fp32
 // FMAs, so this is the form for what the tensor cores do not take: fp32 and
 // other widths.  8 requests of up to 2000 tokens, 4 heads of a small fp32 layer:
-// 13.6 us, which is three launches and their trips to memory.
+// 13 us, which is three launches and their trips to memory.
 #include "paged.cuh"
 #include "sm100.cuh"
 

@@ -45,15 +45,17 @@
 // the boxes of the next but one.  All waits are bounded; a timeout sets the
 // status word.
 //
-// Measured (148 SMs, 64 sequences of 16384 tokens in blocks of 64): 128 heads
-// 285 us, 2.1 PFLOP/s executed in 8 bits; 64 heads 165 us; 16 heads 134 us, 4.5
-// TB/s.  What bounds it: shared memory holds two chunks at 64 heads (2.75 at 16),
-// and a chunk stays from its load's issue until PV frees it, some 3000 cycles of
-// load, 2000-3000 of S, 2000 of softmax and 1500-2500 of PV.  The MMAs of 64 heads
-// take 2280 cycles a chunk of the 4200 (their A operand comes from shared memory
-// at 128 bytes a cycle, which the collector halves for PV's second term); loads
-// alone, without MMAs or softmax, take 116 us of the 134.  Leaving out PV, S,
-// loads or exponentials alone gives 268, 274, 295 and 285 us of 295 at 128 heads.
+// Measured (whole calls of 64 sequences of 16384 tokens in blocks of 64, at an SM
+// clock of 1965 MHz): 128 heads 334 us, 1.7 PFLOP/s executed in 8 bits; 64 heads
+// 186 us; 16 heads 132 us, 4.6 TB/s.  Kept up for a second, the power cap takes the
+// clock to 1.66 GHz: 380, 205 and 132 us.  What bounds it: shared memory holds two
+// chunks at 64 heads (2.75 at 16), and a chunk stays from its load's issue until
+// PV frees it, some 3000 cycles of load, 2000-3000 of S, 2000 of softmax and
+// 1500-2500 of PV.  The MMAs of 64 heads take 2280 cycles a chunk of the 4200
+// (their A operand comes from shared memory at 128 bytes a cycle, which the
+// collector halves for PV's second term); loads alone, without MMAs or softmax,
+// take 0.87 of the time at 16 heads.  Leaving out PV, S, loads or exponentials
+// alone gave 268, 274, 295 and 285 us of 295 at 128.
 // Measured and not kept: two sets of softmax warps on alternate chunks (377 us
 // for 291), four loading warps (16 heads 2 % faster, 48 heads 9 % slower for
 // want of registers), waits by one lane or without a pause between tries (5-10 %
