@@ -53,9 +53,9 @@
 // PV frees it, some 3000 cycles of load, 2000-3000 of S, 2000 of softmax and
 // 1500-2500 of PV.  The MMAs of 64 heads take 2280 cycles a chunk of the 4200
 // (their A operand comes from shared memory at 128 bytes a cycle, which the
-// collector halves for PV's second term); loads alone, without MMAs or softmax,
-// take 0.87 of the time at 16 heads.  Leaving out PV, S, loads or exponentials
-// alone gave 268, 274, 295 and 285 us of 295 at 128.
+// collector halves for PV's second term); at 16 heads loads alone, without MMAs
+// or softmax, take 121 us of 131 between events.  Leaving out PV, S, loads or
+// exponentials alone gave 268, 274, 295 and 285 us of 295 at 128 heads.
 // Measured and not kept: two sets of softmax warps on alternate chunks (377 us
 // for 291), four loading warps (16 heads 2 % faster, 48 heads 9 % slower for
 // want of registers), waits by one lane or without a pause between tries (5-10 %
