@@ -511,7 +511,8 @@ MLA_API size_t mla_decode_paged_workspace_size(const mla_config* cfg, int32_t B,
  * sums are fp32 and out is rounded once.  On tensor cores what multiplies the
  * bytes is a sum of two e4m3 terms, 8 significant bits as bf16 has:
  *   [q_lat | q_pe] of a head to 2^-8 of each value, or 2^-17 of the head's
- *     largest where that is more;
+ *     largest where that is more (a score moves accordingly, as with a bf16
+ *     query: by about one where scores reach hundreds);
  *   a weight times its block's scale, p_j 2^e, to 2^-8 + 2^-11 of itself, or
  *     2^-17 of the largest among the 32 tokens 32 k .. 32 k + 31 of the request
  *     where that is more.  (Blocks of 16 share such a group: rows whose p_j 2^e

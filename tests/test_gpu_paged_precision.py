@@ -70,3 +70,38 @@ def test_blocks_of_scales_far_apart(cuda, heads, bs, gap):
     bound = w_uv @ d_lat + 2.0 ** -8 * np.abs(want)
     err = np.abs(f64(out).reshape(heads, 128) - want)
     assert (err <= bound).all(), (err / bound).max()
+
+
+def eight_bits(q):
+    """A vector as two e4m3 terms and a power of two."""
+    e = np.ceil(np.log2(np.abs(q).max() / 448))
+    s = q / 2.0 ** e
+    hi = O.E4M3[O.to_e4m3(s)]
+    return (hi + O.E4M3[O.to_e4m3(s - hi)]) * 2.0 ** e
+
+
+@pytest.mark.parametrize("bs", [16, 64])
+@pytest.mark.parametrize("heads,dn,dv", [(3, 128, 128), (17, 64, 72), (5, 200, 136)])
+def test_scores_of_hundreds(cuda, heads, dn, dv, bs):
+    """Where scores reach hundreds the query's 8 significant bits decide what the
+    weights are: the output is that of the stated query, to the tolerance of the
+    other bf16 decodes (the weights' rounding 2^-8, the output's 2^-8, and fp32
+    scores: 400 2^-24 a rounding)."""
+    cfg = bf16(heads, qk_nope_head_dim=dn, v_head_dim=dv, softmax_scale=0.15)
+    ctx = [700, 1, 90, 333]
+    d = decode_inputs(cfg, ctx, bs, heads, spread=5.0)
+    d["q_nope"] *= 4
+    d["q_pe"] *= 4
+    out, _ = run_decode_paged(cfg, d, bs)
+    w = f64(d["w"]).reshape(heads, dn + dv, 512)
+    want, top = np.zeros((len(ctx), heads, dv)), 0.0
+    for b in range(len(ctx)):
+        c = O.rows_of(d["cache"].numpy(), d["scales"].numpy(), d["table"], ctx, b, bs)
+        for h in range(heads):
+            q = np.concatenate([f64(d["q_nope"])[b, h] @ w[h, :dn], f64(d["q_pe"])[b, h]])
+            s = cfg.softmax_scale * (c @ eight_bits(q))
+            top = max(top, np.abs(s).max())
+            p = np.exp(s - s.max())
+            want[b, h] = w[h, dn:] @ ((p / p.sum()) @ c[:, :512])
+    assert top > 100
+    assert oracle.max_rel_err(out, want.reshape(len(ctx), -1)) <= 2e-2
