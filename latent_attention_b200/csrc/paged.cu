@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, int alon
     }
     for (int i = t; i < s.tg; i += kPlanThreads) look(given(a, s, i));
   }
-  const bool broken_id = __syncthreads_or(bad_id), ok = fits && !broken_id;
+  const bool broken_id = __syncthreads_or(bad_id) && fits, ok = fits && !broken_id;
   if (!ok) s.ta = s.tg = s.tn = 0;
   for (int b = b0; b < b1; ++b) {
     a.cu[b + 1] = ok ? s.new_end[b] : 0;

@@ -45,8 +45,13 @@ def test_ids_that_the_step_does_not_use_are_not_looked_at(cuda):
     assert check_plan(ctx, new, table, ring, state, bs, 4000)["status"] == "ok"
 
 
-def test_too_few_blocks_come_before_a_bad_id(cuda):
+@pytest.mark.parametrize("where", ["ring", "leaving", "part-filled"])
+@pytest.mark.parametrize("capacity", [2048, 4000])
+def test_too_few_blocks_come_before_a_bad_id(cuda, capacity, where):
     """What does not fit is reported as such; the ids are then not looked at."""
     ctx, new, table, ring, state, bs, n = step(2)
-    ring[state[0]] = -1
-    assert check_plan(ctx, new, table, ring, [state[0], 3], bs, 4000)["status"] == "blocks"
+    if where == "ring":
+        ring[state[0]] = -1
+    else:
+        table[(2, 2) if where == "leaving" else (0, 0)] = -1
+    assert check_plan(ctx, new, table, ring, [state[0], 3], bs, capacity)["status"] == "blocks"
